@@ -6,6 +6,13 @@ The three calls of the C ABI (include/sage.h) keep their names:
     sage_quant_v(v, ...)       V smoothing + per-channel E4M3, transposed
     sage_attn_fwd(...)         INT8 QK^T / FP8 PV attention, FP32 online softmax
 
+and so do the serving calls beside them:
+
+    sage_rope(q, k, ...)       rotary positions (both layouts, partial, scaled)
+    sage_kv_write(k, v, ...)   quantized paged KV cache: write, sage_kv_read back
+    sage_attn_prompt(...)      causal attention over packed prompts, grouped heads
+    sage_attn_token(...)       attention of single tokens over the cache
+
 This module only marshals arguments: torch tensors provide device memory and
 the current CUDA stream; every step of the computation runs in the library's
 CUDA kernels.  Importing it loads libsage.so and raises ImportError if the
@@ -32,7 +39,8 @@ STATUS_NAMES = {0: "SAGE_OK", 1: "SAGE_ERR_INVALID_ARG", 2: "SAGE_ERR_UNSUPPORTE
 EXPORTED = ("sage_npad", "sage_workspace_bytes", "sage_quant_qk", "sage_quant_v", "sage_attn_fwd",
             "sage_check", "sage_set_wait_timeout_ns", "sage_selftest_wait_timeout", "sage_last_error",
             "sage_quant_qk_static", "sage_quant_qk_normrope", "sage_fp8_quant_rows", "sage_fp8_linear",
-            "sage_quant_qkv", "sage_attn_fwd_p_codes")
+            "sage_quant_qkv", "sage_attn_fwd_p_codes", "sage_rope_plan_init", "sage_rope", "sage_kv_write",
+            "sage_kv_read", "sage_attn_prompt", "sage_attn_token", "sage_attn_token_workspace_bytes")
 QK_STATIC_SCRATCH_BYTES = 8 << 20
 
 
@@ -49,6 +57,43 @@ class SageShape(ctypes.Structure):
 class SageNormRope(ctypes.Structure):
     _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("rope_cos", ctypes.c_void_p),
                 ("rope_sin", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+ROPE_MAX_PAIRS = 128
+ROPE_SCALING = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}   # sage_rope_scaling
+DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}           # sage_dtype
+KV_FORMAT = {torch.int8: 0, torch.float8_e4m3fn: 1, torch.uint8: 1}        # sage_kv_format, by the codes' type
+
+
+class SageRows(ctypes.Structure):
+    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("H", ctypes.c_int),
+                ("in_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
+class SageRopePlan(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("mscale", ctypes.c_float), ("turns", ctypes.c_double * ROPE_MAX_PAIRS),
+                ("axis", ctypes.c_ubyte * ROPE_MAX_PAIRS)]
+
+
+class SageKvCache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("D", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+class SagePrompt(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int), ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p), ("Hq", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("D", ctypes.c_int), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("causal", ctypes.c_int), ("sm_scale", ctypes.c_float)]
+
+
+class SageToken(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("q_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("dtype", ctypes.c_int), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p), ("max_len", ctypes.c_int),
+                ("sm_scale", ctypes.c_float)]
 
 
 _vp = ctypes.c_void_p
@@ -79,6 +124,25 @@ _lib.sage_attn_fwd.restype = ctypes.c_int
 _lib.sage_attn_fwd_p_codes.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, SageShape, ctypes.c_float, _vp,
                                        ctypes.c_int, _vp, _vp, _vp]
 _lib.sage_attn_fwd_p_codes.restype = ctypes.c_int
+_lib.sage_rope_plan_init.argtypes = [ctypes.POINTER(SageRopePlan), ctypes.c_int, ctypes.c_int, ctypes.c_double,
+                                     ctypes.c_int, ctypes.c_double, ctypes.c_int, ctypes.c_double, ctypes.c_double,
+                                     ctypes.c_char_p]
+_lib.sage_rope_plan_init.restype = ctypes.c_int
+_lib.sage_rope.argtypes = [SageRows, SageRows, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp,
+                           ctypes.POINTER(SageRopePlan), ctypes.c_int, _vp]
+_lib.sage_rope.restype = ctypes.c_int
+_lib.sage_kv_write.argtypes = [_vp, _vp, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, _vp,
+                               SageKvCache, _vp]
+_lib.sage_kv_write.restype = ctypes.c_int
+_lib.sage_kv_read.argtypes = [SageKvCache, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                              _vp]
+_lib.sage_kv_read.restype = ctypes.c_int
+_lib.sage_attn_prompt.argtypes = [_vp, _vp, _vp, ctypes.POINTER(SagePrompt), _vp, _vp, _vp]
+_lib.sage_attn_prompt.restype = ctypes.c_int
+_lib.sage_attn_token_workspace_bytes.argtypes = [ctypes.c_int] * 5
+_lib.sage_attn_token_workspace_bytes.restype = ctypes.c_size_t
+_lib.sage_attn_token.argtypes = [_vp, ctypes.POINTER(SageToken), SageKvCache, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.sage_attn_token.restype = ctypes.c_int
 _lib.sage_check.argtypes = [_vp]
 _lib.sage_check.restype = ctypes.c_int
 _lib.sage_set_wait_timeout_ns.argtypes = [ctypes.c_int64]
@@ -232,6 +296,261 @@ def set_wait_timeout_ns(ns: int) -> None:
 
 def selftest_wait_timeout(timeout_ns: int, stream=None) -> None:
     _ok(_lib.sage_selftest_wait_timeout(int(timeout_ns), _stream(stream)), "sage_selftest_wait_timeout")
+
+
+# ------------------------------------------------------------------ serving calls
+def _same_device(name, first, *rest):
+    """The one CUDA device of a call's tensors (None among them is skipped)."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: tensors must be on a CUDA device (got {dev})")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+    return dev
+
+
+def _row_stride(name, t, H, D):
+    """Token stride of rows [T, H, D] whose heads are contiguous (0 where there is one row at most)."""
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D:
+        raise ValueError(f"{name} must be [T, {H}, {D}] (got {tuple(t.shape)})")
+    st = t.stride()
+    if t.numel() and (st[2] != 1 or (H > 1 and st[1] != D)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {st})")
+    return st[0] if t.shape[0] > 1 else 0
+
+
+def _row_dtype(name, t, *rest):
+    code = DTYPE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: dtype {t.dtype} is not one of {list(DTYPE)}")
+    for r in rest:
+        if r is not None and r.dtype != t.dtype:
+            raise TypeError(f"{name}: {r.dtype} beside {t.dtype}")
+    return code
+
+
+def _int_vector(name, t, n, dtype):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}] (got {t.dtype} {tuple(t.shape)})")
+
+
+def _launch(dev, stream, call, where):
+    """Runs call(stream pointer) with the tensors' device current, on the given stream or that device's current one."""
+    if dev.index == torch.cuda.current_device():
+        status = call(torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = call(_stream(stream))
+    if status != SAGE_OK:
+        raise SageError(status, where)
+
+
+class RopePlan:
+    """Rotation per position of every channel pair (sage_rope_plan).
+
+    rot_dim channels of each head turn; interleaved pairs (2i, 2i+1), else halves (i, i + rot_dim/2).
+    scaling: None, "linear", "ntk" or "yarn" for a context `factor` times longer than orig_len.  axis: position
+    axis of each pair (positions are then [axes, T]).  inv_freq: radians per position of each pair, in place of
+    base and scaling; mscale: factor on cos and sin, in place of the scaling's."""
+
+    def __init__(self, rot_dim, base=10000.0, interleaved=False, scaling=None, factor=1.0, orig_len=0, beta_fast=32.0,
+                 beta_slow=1.0, axis=None, inv_freq=None, mscale=None):
+        self.struct = SageRopePlan()
+        if axis is not None and len(axis) != rot_dim // 2:
+            raise ValueError(f"axis must name {rot_dim // 2} pairs (got {len(axis)})")
+        if scaling not in ROPE_SCALING:
+            raise ValueError(f"scaling must be one of {list(ROPE_SCALING)} (got {scaling!r})")
+        _ok(_lib.sage_rope_plan_init(ctypes.byref(self.struct), rot_dim, int(bool(interleaved)), float(base),
+                                     ROPE_SCALING[scaling], float(factor), int(orig_len), float(beta_fast),
+                                     float(beta_slow), None if axis is None else bytes(int(a) for a in axis)),
+            "sage_rope_plan_init")
+        if inv_freq is not None:
+            if len(inv_freq) != rot_dim // 2:
+                raise ValueError(f"inv_freq must hold {rot_dim // 2} values (got {len(inv_freq)})")
+            for i, f in enumerate(inv_freq):
+                self.struct.turns[i] = float(f) / 6.283185307179586
+        if mscale is not None:
+            self.struct.mscale = float(mscale)
+        self._ref = ctypes.byref(self.struct)
+
+    n_axes = property(lambda self: self.struct.n_axes)
+    rot_dim = property(lambda self: self.struct.rot_dim)
+
+
+def sage_rope(q, k, positions, plan, q_out=None, k_out=None, transpose=False, stream=None):
+    """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (either may be None) in one launch.  positions: int64 [T], or
+    [axes, T].  In place without q_out / k_out.  transpose: the gradient of the rotation.  Returns (q_out, k_out)."""
+    x = q if q is not None else k
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    dev = _same_device("sage_rope", x, k, q_out, k_out, positions)
+    dt = _row_dtype("sage_rope", x, k, q_out, k_out)
+    T, D = x.shape[0], x.shape[2] if x.dim() == 3 else 0
+    rows = []
+    for name, a, b in (("q", q, q_out), ("k", k, k_out)):
+        if a is None:
+            rows.append(SageRows(None, None, 0, 0, 0))
+            continue
+        if a.dim() != 3 or a.shape[0] != T or b.shape != a.shape:
+            raise ValueError(f"{name} and {name}_out must be [{T}, H, {D}] (got {tuple(a.shape)}, {tuple(b.shape)})")
+        H = a.shape[1]
+        rows.append(SageRows(a.data_ptr(), b.data_ptr(), H, _row_stride(name, a, H, D), _row_stride(name + "_out", b, H, D)))
+    n = plan.struct.n_axes
+    if positions.dtype != torch.int64 or positions.numel() != n * T or positions.shape[-1] != T \
+            or not positions.is_contiguous():
+        raise ValueError(f"positions must be contiguous int64 [{T}] or [{n}, {T}] (got {positions.dtype} "
+                         f"{tuple(positions.shape)})")
+    _launch(dev, stream, lambda st: _lib.sage_rope(rows[0], rows[1], T, D, dt, positions.data_ptr(), plan._ref,
+                                                   int(bool(transpose)), st), "sage_rope")
+    return q_out, k_out
+
+
+def _cache(name, k_codes, k_scale, v_codes, v_scale):
+    """sage_kv_cache of codes [pages, Hk, page_size, D] (int8, or float8_e4m3fn / uint8) and float32 scales
+    [pages, Hk, page_size]."""
+    fmt = KV_FORMAT.get(k_codes.dtype)
+    if fmt is None or v_codes.dtype != k_codes.dtype:
+        raise TypeError(f"{name}: codes must both be int8, float8_e4m3fn or uint8 (got {k_codes.dtype}, {v_codes.dtype})")
+    shape = k_codes.shape
+    if len(shape) != 4 or v_codes.shape != shape or k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+        raise ValueError(f"{name}: codes must be [pages, Hk, page_size, D] and scales [pages, Hk, page_size] (got "
+                         f"{tuple(shape)}, {tuple(v_codes.shape)}, {tuple(k_scale.shape)}, {tuple(v_scale.shape)})")
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise TypeError(f"{name}: scales must be float32")
+    if not (k_codes.is_contiguous() and v_codes.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous()):
+        raise ValueError(f"{name}: the cache must be contiguous")
+    return SageKvCache(k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(), v_scale.data_ptr(), shape[0],
+                       shape[2], shape[1], shape[3], fmt)
+
+
+def _kv_rows(name, k, v, slots, c):
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"{name}: k and v have {T} and {v.shape[0]} rows")
+    _int_vector(f"{name}: slots", slots, T, torch.int64)
+    return T, _row_stride("k", k, c.Hk, c.D), _row_stride("v", v, c.Hk, c.D), _row_dtype(name, k, v)
+
+
+def sage_kv_write(k, v, slots, k_codes, k_scale, v_codes, v_scale, stream=None):
+    """Quantizes the rows of k, v [T, Hk, D] into the cache slots (int64 [T]; page * page_size + offset; a negative
+    slot's row is not written)."""
+    dev = _same_device("sage_kv_write", k, v, slots, k_codes, k_scale, v_codes, v_scale)
+    c = _cache("sage_kv_write", k_codes, k_scale, v_codes, v_scale)
+    T, ks, vs, dt = _kv_rows("sage_kv_write", k, v, slots, c)
+    _launch(dev, stream, lambda st: _lib.sage_kv_write(k.data_ptr(), v.data_ptr(), T, ks, vs, dt, slots.data_ptr(), c,
+                                                       st), "sage_kv_write")
+
+
+def sage_kv_read(slots, k_codes, k_scale, v_codes, v_scale, k, v, stream=None):
+    """Dequantizes the cache slots (int64 [T]) into k, v [T, Hk, D]; rows of negative slots keep their contents."""
+    dev = _same_device("sage_kv_read", k, v, slots, k_codes, k_scale, v_codes, v_scale)
+    c = _cache("sage_kv_read", k_codes, k_scale, v_codes, v_scale)
+    T, ks, vs, dt = _kv_rows("sage_kv_read", k, v, slots, c)
+    _launch(dev, stream, lambda st: _lib.sage_kv_read(c, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), ks, vs, dt,
+                                                      st), "sage_kv_read")
+    return k, v
+
+
+def _offsets(name, cu, total):
+    if isinstance(cu, torch.Tensor):
+        if cu.is_cuda:
+            raise ValueError(f"{name} must be on the host (a list or a CPU tensor)")
+        cu = cu.tolist()
+    if len(cu) < 1 or cu[-1] != total:
+        raise ValueError(f"{name} must end at the {total} packed rows (got {list(cu)[-1:]})")
+    return (ctypes.c_int32 * len(cu))(*cu)
+
+
+def sage_attn_prompt(q, k, v, cu_q, cu_k=None, out=None, lse=None, causal=True, sm_scale=0.0, stream=None):
+    """Attention over packed sequences: q [Tq, Hq, D], k, v [Tk, Hk, D] BF16 or FP16; cu_q, cu_k host offsets (cu_k None:
+    cu_q).  causal: query i of a sequence sees keys j <= i + Lk - Lq.  lse: float32 [Hq, Tq] or None.  Returns out."""
+    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+    dev = _same_device("sage_attn_prompt", q, k, v, out, lse)
+    dt = _row_dtype("sage_attn_prompt", q, k, v, out)
+    if q.dim() != 3 or k.dim() != 3 or out.shape != q.shape or k.shape != v.shape:
+        raise ValueError(f"sage_attn_prompt: q, out [Tq, Hq, D] and k, v [Tk, Hk, D] are wanted (got {tuple(q.shape)}, "
+                         f"{tuple(out.shape)}, {tuple(k.shape)}, {tuple(v.shape)})")
+    Tq, Hq, D = q.shape
+    Hk = k.shape[1]
+    cq = _offsets("cu_q", cu_q, Tq)
+    ck = _offsets("cu_k", cu_q if cu_k is None else cu_k, k.shape[0])
+    if len(ck) != len(cq):
+        raise ValueError(f"cu_q and cu_k name {len(cq) - 1} and {len(ck) - 1} sequences")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (Hq, Tq) or not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous float32 [{Hq}, {Tq}]")
+    p = SagePrompt(len(cq) - 1, ctypes.addressof(cq), ctypes.addressof(ck), Hq, Hk, D, _row_stride("q", q, Hq, D),
+                   _row_stride("k", k, Hk, D), _row_stride("v", v, Hk, D), _row_stride("out", out, Hq, D), dt,
+                   int(bool(causal)), float(sm_scale))
+    _launch(dev, stream, lambda st: _lib.sage_attn_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(p),
+                                                          out.data_ptr(), _ptr(lse), st), "sage_attn_prompt")
+    return out
+
+
+def attn_token_workspace_bytes(B, Hq, Hk, D, max_len) -> int:
+    return int(_lib.sage_attn_token_workspace_bytes(int(B), int(Hq), int(Hk), int(D), int(max_len)))
+
+
+def sage_attn_token(q, k_codes, k_scale, v_codes, v_scale, page_table, lens, out, workspace, max_len=None, lse=None,
+                    sm_scale=0.0, stream=None):
+    """Attention of one token per sequence, q [B, Hq, D] BF16 or FP16, over the cache: page_table int32 [B, pages],
+    lens int32 [B] (keys seen).  max_len: upper bound on lens (None: what the table can name).  workspace: at least
+    attn_token_workspace_bytes(...) bytes, kept by the caller.  lse: float32 [B, Hq] or None.  Returns out."""
+    dev = _same_device("sage_attn_token", q, k_codes, k_scale, v_codes, v_scale, page_table, lens, out, workspace, lse)
+    c = _cache("sage_attn_token", k_codes, k_scale, v_codes, v_scale)
+    dt = _row_dtype("sage_attn_token", q, out)
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError(f"sage_attn_token: q and out must be [B, Hq, D] (got {tuple(q.shape)}, {tuple(out.shape)})")
+    B, Hq, D = q.shape
+    if D != c.D:
+        raise ValueError(f"sage_attn_token: q has D = {D}, the cache {c.D}")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
+            or (page_table.numel() and page_table.stride(1) != 1):
+        raise ValueError(f"page_table must be int32 [{B}, pages], rows contiguous (got {page_table.dtype} "
+                         f"{tuple(page_table.shape)})")
+    _int_vector("lens", lens, B, torch.int32)
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous float32 [{B}, {Hq}]")
+    pages = page_table.shape[1]
+    if max_len is None:
+        max_len = pages * c.page_size
+    elif max_len > pages * c.page_size:
+        raise ValueError(f"max_len {max_len} is above what the page table can name ({pages * c.page_size})")
+    p = SageToken(B, Hq, _row_stride("q", q, Hq, D), _row_stride("out", out, Hq, D), dt, page_table.data_ptr(),
+                  page_table.stride(0) if B > 1 else pages, lens.data_ptr(), max_len, float(sm_scale))
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _launch(dev, stream, lambda st: _lib.sage_attn_token(q.data_ptr(), ctypes.byref(p), c, out.data_ptr(), _ptr(lse),
+                                                         _ptr(workspace), ws_bytes, st), "sage_attn_token")
+    return out
+
+
+class KVCache:
+    """A quantized paged KV cache: int8 or E4M3 codes and a float32 scale per token and KV head."""
+
+    def __init__(self, num_pages, page_size, Hk, D, fmt="int8", device="cuda"):
+        dt = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}.get(fmt)
+        if dt is None:
+            raise ValueError(f"fmt must be 'int8' or 'e4m3' (got {fmt!r})")
+        self.num_pages, self.page_size, self.Hk, self.D, self.fmt = num_pages, page_size, Hk, D, fmt
+        codes, scales = (num_pages, Hk, page_size, D), (num_pages, Hk, page_size)
+        self.k_codes = torch.zeros(codes, dtype=torch.uint8, device=device).view(dt)
+        self.v_codes = torch.zeros(codes, dtype=torch.uint8, device=device).view(dt)
+        self.k_scale = torch.zeros(scales, dtype=torch.float32, device=device)
+        self.v_scale = torch.zeros(scales, dtype=torch.float32, device=device)
+
+    @property
+    def tensors(self):
+        return self.k_codes, self.k_scale, self.v_codes, self.v_scale
+
+    def write(self, k, v, slots, stream=None):
+        sage_kv_write(k, v, slots, *self.tensors, stream=stream)
+
+    def read(self, slots, k, v, stream=None):
+        return sage_kv_read(slots, *self.tensors, k, v, stream=stream)
+
+    def attend(self, q, page_table, lens, out, workspace, max_len=None, lse=None, sm_scale=0.0, stream=None):
+        return sage_attn_token(q, *self.tensors, page_table, lens, out, workspace, max_len, lse, sm_scale, stream)
 
 
 class Buffers:

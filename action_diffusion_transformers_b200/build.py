@@ -2,10 +2,12 @@
 
     python -m action_diffusion_transformers_b200.build [--verbose]
 
-nvcc compiles the single translation unit csrc/sage_api.cu (which includes the
-kernel headers) into a shared library with the CUDA runtime linked statically,
-so the .so loads on a machine without a GPU (for the symbol checks) and on the
-B200 machine alongside torch.
+nvcc compiles csrc/sage_api.cu (quantized attention, projections) and
+csrc/serve_api.cu (rotary positions, KV cache, prompt and single-token
+attention), each with the kernel headers it includes, side by side and links
+them into a shared library with the CUDA runtime linked statically, so the .so
+loads on a machine without a GPU (for the symbol checks) and on the B200 machine
+alongside torch.
 """
 from __future__ import annotations
 
@@ -13,13 +15,14 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsage.so")
-SOURCES = [os.path.join(CSRC, "sage_api.cu")]
+SOURCES = [os.path.join(CSRC, "sage_api.cu"), os.path.join(CSRC, "serve_api.cu")]
 
 
 def deps() -> list:
@@ -50,16 +53,23 @@ def up_to_date() -> bool:
 def build(verbose: bool = False, force: bool = False) -> str:
     if not force and up_to_date():
         return LIB
-    cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-           "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-           "-I", INCLUDE, "-I", CSRC, "-o", LIB + ".tmp"] + SOURCES
+    flags = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
+             "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-    if verbose:
-        sys.stdout.write(r.stdout + r.stderr)
+        flags.insert(0, "-Xptxas=-v")
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SOURCES]
+        cmds = [[nvcc()] + flags + ["-c", "-o", obj, src] for src, obj in zip(SOURCES, objs)]
+        runs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in cmds]
+        for cmd, (out, rc) in zip(cmds, [(r.communicate()[0], r.returncode) for r in runs]):
+            if rc != 0:
+                raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + out)
+            if verbose:
+                sys.stdout.write(out)
+        cmd = [nvcc()] + flags + ["-shared", "-o", LIB + ".tmp"] + objs
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

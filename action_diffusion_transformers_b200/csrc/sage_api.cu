@@ -20,14 +20,19 @@
 #include "sage.h"
 #include "fp8_linear.cuh"
 #include "sage_attn.cuh"
+#include "sage_host.h"
 #include "sage_quant.cuh"
 
 namespace {
 
-__device__ int g_sage_err;  // set to 1 by a kernel that gave up a bounded wait
+__device__ int g_sage_err[2];  // [0] a bounded wait was given up, [1] an index outside a cache
 
 thread_local std::string g_last_error;
 std::atomic<int64_t> g_timeout_ns{2000000000LL};
+
+}  // namespace
+
+namespace sage_host {
 
 sage_status fail(sage_status st, const char* fmt, ...) {
   char buf[512];
@@ -43,7 +48,26 @@ sage_status cuda_fail(cudaError_t e, const char* what) {
   return fail(SAGE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-constexpr int kMaxDevices = 64;
+sage_status launch_check(const char* what) {
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return SAGE_OK;
+}
+
+int64_t wait_timeout_ns() { return g_timeout_ns.load(); }
+
+}  // namespace sage_host
+
+namespace {
+
+using sage_host::aligned16;
+using sage_host::cuda_fail;
+using sage_host::device_setup;
+using sage_host::EncodeTiledFn;
+using sage_host::fail;
+using sage_host::kMaxDevices;
+using sage_host::launch_check;
+using sage_host::pdl_launch;
 
 struct DeviceState {
   bool ready = false;
@@ -55,14 +79,13 @@ struct DeviceState {
 DeviceState g_dev[kMaxDevices];
 std::mutex g_dev_mu;
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
+
+}  // namespace
 
 // Once per device: check for sm_100, look up the error word, raise the shared
 // memory limit of the attention kernels, and find cuTensorMapEncodeTiled.
-sage_status device_setup(int* dev_out, int** err_out, int* sm_count_out = nullptr) {
+sage_status sage_host::device_setup(int* dev_out, int** err_out, int* sm_count_out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -145,7 +168,9 @@ sage_status device_setup(int* dev_out, int** err_out, int* sm_count_out = nullpt
   return SAGE_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+sage_host::EncodeTiledFn sage_host::encode_tiled() { return g_encode; }
+
+namespace {
 
 int64_t npad_of(int N) { return (static_cast<int64_t>(N) + 127) / 128 * 128; }
 
@@ -209,41 +234,6 @@ sage_status check_ws(const sage_shape& s, const void* ws, size_t ws_bytes, WsLay
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(SAGE_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
   if (ws_bytes < need)
     return fail(SAGE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
-  return SAGE_OK;
-}
-
-#define SAGE_NEED(p, name) \
-  do { if (!(p)) return fail(SAGE_ERR_INVALID_ARG, "%s is NULL", name); \
-       if (!aligned16(p)) return fail(SAGE_ERR_ALIGNMENT, "%s is not 16-byte aligned", name); } while (0)
-
-// Launches with programmatic stream serialization allowed: the kernel may be
-// scheduled while the previous kernel in the stream is still running; every
-// kernel of this library begins with pdl_enter(), which waits for that kernel
-// to complete (and its writes to be visible) before anything is read.
-// kEarly = false: an ordinary launch (after the previous kernel has finished),
-// used for the attention kernel: with its blocks scheduled early beside the
-// last quantization pass it measured 0.35% slower on one B200 and the same on
-// another, for a gain of a few microseconds per step at most.
-template <bool kEarly = true, typename... KArgs, typename... Args>
-void pdl_launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = kEarly ? 1 : 0;
-  // A failed launch is also recorded as this thread's last CUDA error, which
-  // launch_check() reads after the call's launches.
-  (void)cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
-sage_status launch_check(const char* what) {
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, what);
   return SAGE_OK;
 }
 
@@ -830,15 +820,17 @@ sage_status sage_check(sage_stream_t stream) {
   if (st != SAGE_OK) return st;
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-  int flag = 0;
-  e = cudaMemcpy(&flag, err, sizeof(int), cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
-  if (flag) {
-    const int zero = 0;
-    e = cudaMemcpy(err, &zero, sizeof(int), cudaMemcpyHostToDevice);
-    if (e != cudaSuccess) return cuda_fail(e, "clearing the device error word");
-    return fail(SAGE_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (timeout %lld ns)",
-                (long long)g_timeout_ns.load());
+  int flag[2] = {0, 0};
+  e = cudaMemcpy(flag, err, sizeof(flag), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return cuda_fail(e, "reading the device error words");
+  if (flag[0] || flag[1]) {
+    const int zero[2] = {0, 0};
+    e = cudaMemcpy(err, zero, sizeof(zero), cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) return cuda_fail(e, "clearing the device error words");
+    if (flag[0])
+      return fail(SAGE_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (timeout %lld ns)",
+                  (long long)g_timeout_ns.load());
+    return fail(SAGE_ERR_INVALID_ARG, "a kernel met a slot or page index outside the cache and skipped it");
   }
   return SAGE_OK;
 }

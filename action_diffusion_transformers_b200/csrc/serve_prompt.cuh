@@ -1,0 +1,462 @@
+// serve_prompt.cuh - softmax attention over packed prompts on sm_100a tensor
+// cores, 16-bit operands:
+//   O_i = sum_{j visible} 2^(x_ij - m_i) v_j / sum_j 2^(x_ij - m_i),
+//   x_ij = (q_i . k_j) * sm_scale * log2 e,
+// key j of a sequence visible to its query i when j <= i + Lk - Lq (causal,
+// aligned at the end) or always; grouped heads; sequences packed row after
+// row, their bounds given by the host.
+//
+// One CTA takes 256 query rows (two tiles of 128, A and B) of one (sequence,
+// head), 320 threads:
+//   warps 0-3, 4-7  softmax of tile A, of tile B: thread r owns query row r
+//                   (TMEM lane r), reads its 128 scores, writes P back as
+//                   16-bit pairs over the first 64 score columns, rescales its
+//                   row of O when the reference m moves, and stores the row.
+//   warp 8          MMA: S = Q K^T (shared x shared), O += P V (P in TMEM).
+//   warp 9          TMA loads: Q once, K and V tiles of 128 keys into a ring.
+// TMEM (512 columns): S_A, S_B at 0, 128; O_A, O_B at 256, 384.
+// While tile A's softmax runs, the tensor core works on tile B and the other
+// way round.  S_X(j+1) overwrites the columns that PV_X(j) reads P from, so it
+// is issued only after PV_X(j) has completed; a softmax thread that sees
+// S_X(j) therefore knows that O_X holds every product up to j - 1.
+//
+// The reference m of a row moves only when a score passes it by 2^8 (P stays
+// below 2^8 in 16 bits and the sums in 32 bits), so O is rescaled rarely.  P is
+// rounded to the operands' 16-bit type (bf16 2^-9 relative, fp16 2^-12, each
+// weight on its own): the tensor core multiplies equal types.  The row sum adds
+// the weights before that rounding; sums, references and O stay in 32 bits.
+//
+// Values in masked places: a masked score is replaced, never added to, so K may
+// hold anything there.  A masked weight is 0, but 0 times an infinity or a NaN
+// in a masked V row (a later token, another sequence's row in the same tile)
+// would spread to the row's output; a row whose output is not finite is
+// therefore computed once more from its visible keys alone, in 32 bits.
+//
+// Every wait is bounded (see mbar_wait_bounded), as in sage_attn.cuh.
+#pragma once
+#include "serve_rows.cuh"
+#include "serve_token.cuh"
+
+namespace sage {
+
+constexpr int kPrTile = 128;
+constexpr int kPrThreads = 320;
+constexpr int kPrMaxSeq = 256;          // sequences per launch
+constexpr float kPrRaise = 8.f;
+
+template <int D>
+struct PrSmem {
+  static constexpr int kTileBytes = kPrTile * D * 2;
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kQ = 0;                                // A, B
+  static constexpr int kRing = 2 * kTileBytes;
+  static constexpr int kBar = kRing + kSlots * kTileBytes;
+  // q[2], s_full[2], p_full[2], pv_done[2], full[], empty[], drain
+  static constexpr int kQFull = 0, kSFull = 2, kPFull = 4, kPVDone = 6, kFull = 8, kEmpty = 8 + kSlots,
+                       kDrain = 8 + 2 * kSlots, kNumBars = 9 + 2 * kSlots;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kTotal = kMisc + 16;
+  static constexpr int kAlloc = kTotal + 1024;
+};
+static_assert(PrSmem<128>::kAlloc <= 232448 && PrSmem<64>::kAlloc <= 232448, "shared memory of one CTA");
+
+struct PromptSeq {
+  int q0, k0, lq, lk;       // first rows and lengths
+};
+
+struct PromptParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;               // [Hq, Tq] or null
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  int64_t lse_stride;       // Tq
+  int Hq, G, n_seq, causal;
+  float scale_log2;
+  int* err;
+  int64_t timeout_ns;
+  PromptSeq seq[kPrMaxSeq];
+  int tile_end[kPrMaxSeq];  // CTA tiles (256 rows) up to and including a sequence
+};
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Descriptor of an operand whose rows (128-byte swizzled, 8-row groups of 1024
+// bytes) run along the product's K axis and whose 64-element row pieces lie
+// `piece` bytes apart (V: keys are rows, channels are contiguous).
+__device__ __forceinline__ uint64_t make_sdesc_mn(uint32_t saddr, uint32_t piece) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((piece & 0x3FFFFu) >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// A softmax warp stays whole in front of its warp-wide TMEM accesses.
+__device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int64_t tmo) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, tmo));
+}
+
+// One row once more from its visible keys, channel by channel group, in 32
+// bits: only for rows whose first result was not finite.
+template <class E, int D>
+__device__ __noinline__ void prompt_row_again(const PromptParams& p, const PromptSeq& sq, int row, int h, int visible,
+                                              float m, float rl) {
+  using S = typename E::S;
+  const S* q = static_cast<const S*>(p.q) + static_cast<int64_t>(sq.q0 + row) * p.q_stride + static_cast<int64_t>(h) * D;
+  const int64_t hk = static_cast<int64_t>(h / p.G) * D;
+  S* out = static_cast<S*>(p.out) + static_cast<int64_t>(sq.q0 + row) * p.out_stride + static_cast<int64_t>(h) * D;
+  for (int d = 0; d < D; d += 8) {
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < visible; ++j) {
+      const S* k = static_cast<const S*>(p.k) + static_cast<int64_t>(sq.k0 + j) * p.k_stride + hk;
+      const S* v = static_cast<const S*>(p.v) + static_cast<int64_t>(sq.k0 + j) * p.v_stride + hk;
+      float s = 0.f;
+      for (int c = 0; c < D; c += 8) {
+        Piece<E, 8> a, b;
+        float x[8], y[8];
+        a.load(q + c);
+        b.load(k + c);
+        a.get(x);
+        b.get(y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+      }
+      const float w = ex2_approx(fmaf(s, p.scale_log2, -m));
+      Piece<E, 8> a;
+      float x[8];
+      a.load(v + d);
+      a.get(x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = fmaf(w, x[i], o[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= rl;
+    Piece<E, 8> r;
+    r.put(o);
+    r.store(out + d);
+  }
+}
+
+template <class E, int D>
+__global__ void __launch_bounds__(kPrThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PromptParams p) {
+  pdl_enter();
+  using L = PrSmem<D>;
+  using S = typename E::S;
+  constexpr int kSlots = L::kSlots;
+  constexpr bool kBf16 = std::is_same<E, Bf16T>::value;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t tmo = p.timeout_ns;
+
+  // CTA -> (tile of 256 rows, head): heads run fastest; the tiles of a sequence
+  // run from its end (most visible keys) to its start.
+  const int tile = blockIdx.x / p.Hq;
+  const int h = blockIdx.x - tile * p.Hq;
+  int lo = 0, hi = p.n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (tile < p.tile_end[mid]) hi = mid;
+    else lo = mid + 1;
+  }
+  const PromptSeq sq = p.seq[lo];
+  const int row0 = (p.tile_end[lo] - 1 - tile) * 2 * kPrTile;
+  // Keys that the last row of each tile sees, and the key tiles this makes.
+  const int off = sq.lk - sq.lq;
+  int nt[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int a = row0 + x * kPrTile;
+    const int last = min(a + kPrTile, sq.lq) - 1;
+    const int seen = p.causal ? min(sq.lk, last + off + 1) : sq.lk;
+    nt[x] = a < sq.lq && seen > 0 ? (seen + kPrTile - 1) / kPrTile : 0;
+  }
+  const int n = max(nt[0], nt[1]);
+
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < L::kNumBars; ++i)
+      mbar_init(&bars[i], i == L::kPFull || i == L::kPFull + 1 ? kPrTile : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 9) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0 && n > 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+      const int hk = h / p.G;
+      auto load = [&](uint8_t* dst, const CUtensorMap* tm, int head, int row, uint64_t* bar) {
+        mbar_arrive_expect_tx(bar, L::kTileBytes);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * kPrTile * 128, tm, c * 64, head, row, bar);
+      };
+      int issued = 0;
+      for (int it = 0; it < 2 * n; ++it) {
+        const int slot = it % kSlots;
+        const uint32_t use = static_cast<uint32_t>(it / kSlots);
+        if (it == 0 && nt[0] > 0) load(smem + L::kQ, &tm_q, h, sq.q0 + row0, &bars[L::kQFull]);
+        if (use > 0 && !mbar_wait_bounded(&bars[L::kEmpty + slot], (use - 1) & 1, abort_flag, tmo)) break;
+        load(smem + L::kRing + slot * L::kTileBytes, (it & 1) ? &tm_v : &tm_k, hk, sq.k0 + (it >> 1) * kPrTile,
+             &bars[L::kFull + slot]);
+        issued = it + 1;
+        if (it == 0 && nt[1] > 0)
+          load(smem + L::kQ + L::kTileBytes, &tm_q, h, sq.q0 + row0 + kPrTile, &bars[L::kQFull + 1]);
+      }
+      if (*abort_flag) {
+        // Wait (bounded) for the loads in flight: Q and the last one of each slot.
+        const int64_t drain = 200000000;
+        int none = 0;
+        volatile int* nf = reinterpret_cast<volatile int*>(&none);
+        if (nt[0] > 0) mbar_wait_bounded(&bars[L::kQFull], 0, nf, drain);
+        if (nt[1] > 0) mbar_wait_bounded(&bars[L::kQFull + 1], 0, nf, drain);
+        for (int slot = 0; slot < kSlots && slot < issued; ++slot) {
+          const int last = (issued - 1 - slot) / kSlots;
+          mbar_wait_bounded(&bars[L::kFull + slot], static_cast<uint32_t>(last) & 1, nf, drain);
+        }
+      }
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t kFmt = kBf16 ? 1u : 0u;
+      constexpr uint32_t kIdescQK = make_idesc(1u, kFmt, 128u, 128u);
+      constexpr uint32_t kIdescPV = make_idesc(1u, kFmt, 128u, static_cast<uint32_t>(D)) | (1u << 16);
+      auto wait = [&](int bar, int phase) {
+        return mbar_wait_bounded(&bars[bar], static_cast<uint32_t>(phase) & 1, abort_flag, tmo);
+      };
+      auto slot_of = [&](int it) { return it % kSlots; };
+      auto wait_full = [&](int it) { return wait(L::kFull + slot_of(it), it / kSlots); };
+      auto scores = [&](int x, int j) {           // S_x(j) = Q_x K_j^T
+        const uint64_t qd = make_sdesc(smem_u32(smem + L::kQ + x * L::kTileBytes), 1024u, 2u);
+        const uint64_t kd = make_sdesc(smem_u32(smem + L::kRing + slot_of(2 * j) * L::kTileBytes), 1024u, 2u);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t step = (kk & 3) * 2 + (kk >> 2) * (kPrTile * 128 / 16);
+          mma_f16_ss(tmem + x * 128, qd + step, kd + step, kIdescQK, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&bars[L::kSFull + x]);
+      };
+      auto products = [&](int x, int j) {         // O_x += P_x(j) V_j
+        const uint64_t vd =
+            make_sdesc_mn(smem_u32(smem + L::kRing + slot_of(2 * j + 1) * L::kTileBytes), kPrTile * 128);
+#pragma unroll
+        for (int kk = 0; kk < kPrTile / 16; ++kk)
+          mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, vd + kk * (16 * 128 / 16), kIdescPV,
+                     (j > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(&bars[L::kPVDone + x]);
+      };
+      bool ok = wait_full(0);
+      for (int x = 0; x < 2 && ok; ++x)
+        if (nt[x] > 0) {
+          ok = wait(L::kQFull + x, 0);
+          if (ok) {
+            tc_fence_after();
+            scores(x, 0);
+          }
+        }
+      if (ok) tc_commit(&bars[L::kEmpty + slot_of(0)]);
+      for (int j = 0; ok && j < n; ++j) {
+        if (!(ok = wait_full(2 * j + 1))) break;
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (j < nt[x]) {
+            if (!(ok = wait(L::kPFull + x, j))) break;
+            tc_fence_after();
+            products(x, j);
+            if (j + 1 < nt[x]) {
+              // S_x(j+1) takes the columns that hold P_x(j): wait for its products.
+              if (!(ok = wait_full(2 * j + 2) && wait(L::kPVDone + x, j))) break;
+              tc_fence_after();
+              scores(x, j + 1);
+            }
+          }
+        }
+        if (!ok) break;
+        // Completes when all that was issued so far has, so V_j and K_j+1 are read.
+        tc_commit(&bars[L::kEmpty + slot_of(2 * j + 1)]);
+        if (j + 1 < n) tc_commit(&bars[L::kEmpty + slot_of(2 * j + 2)]);
+      }
+      tc_commit(&bars[L::kDrain]);
+      int none = 0;
+      mbar_wait_bounded(&bars[L::kDrain], 0, reinterpret_cast<volatile int*>(&none), 200000000);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int x = warp >> 2;                       // tile A, B
+    const int r = tid & 127;
+    const int row = row0 + x * kPrTile + r;        // of the sequence
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + x * 128 + lane_base;
+    const uint32_t to = tmem + 256 + x * 128 + lane_base;
+    const float kNegInf = -__int_as_float(0x7F800000);
+    const float sl = p.scale_log2;
+    const int visible = p.causal ? min(sq.lk, max(0, row + off + 1)) : sq.lk;
+    float m = kNegInf;                             // reference, log2 units
+    float l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < nt[x]; ++j) {
+      if (!(ok = pr_wait(&bars[L::kSFull + x], static_cast<uint32_t>(j) & 1, abort_flag, tmo))) break;
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, s[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) reg_fence(s[c]);
+      const int valid = visible - j * kPrTile;
+      if (__any_sync(0xFFFFFFFFu, valid < kPrTile)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i >= valid) s[c][i] = __float_as_uint(kNegInf);
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int i = 1; i < 31; i += 2)
+          mx[c] = fmax3(mx[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+        mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
+      }
+      const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+      if (__any_sync(0xFFFFFFFFu, tmax > m + kPrRaise)) {
+        const float m1 = fmaxf(m, tmax);
+        const float alpha = m == kNegInf ? 0.f : ex2_approx(m - m1);
+        l *= alpha;
+        m = m1;
+        if (j > 0) {
+          const f32x2_t a2 = x2_splat(alpha);
+#pragma unroll
+          for (int cb = 0; cb < D; cb += 32) {
+            f32x2_t o[16];
+            tmem_ld32_pairs(to + cb, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = x2_mul(o[i], a2);
+            tmem_st32_pairs(to + cb, o);
+          }
+        }
+      }
+      const float ref = m == kNegInf ? 0.f : m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float a = ex2_approx(fmaf(__uint_as_float(s[c][2 * i]), sl, -ref));
+          const float b = ex2_approx(fmaf(__uint_as_float(s[c][2 * i + 1]), sl, -ref));
+          sum[i & 3] += a + b;
+          pk[i] = E::pack(a, b);
+        }
+        tmem_st16(ts + 16 * c, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bars[L::kPFull + x]);
+    }
+    const bool mine = row < sq.lq;
+    S* dst = static_cast<S*>(p.out) + static_cast<int64_t>(sq.q0 + row) * p.out_stride + static_cast<int64_t>(h) * D;
+    if (nt[x] > 0) {
+      if (ok) ok = pr_wait(&bars[L::kPVDone + x], static_cast<uint32_t>(nt[x] - 1) & 1, abort_flag, tmo);
+      if (ok) {
+        tc_fence_after();
+        // No visible key: nothing was added, the row is zeros.
+        const float rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
+        bool finite = true;
+#pragma unroll
+        for (int cb = 0; cb < D; cb += 32) {
+          uint32_t o[32];
+          tmem_ld32(to + cb, o);
+          tmem_wait_ld();
+          reg_fence(o);
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float f[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float v = __uint_as_float(o[8 * i + k]);
+                finite = finite && fabsf(v) < __int_as_float(0x7F800000);
+                f[k] = v * rl;
+              }
+              Piece<E, 8> pc;
+              pc.put(f);
+              pc.store(dst + cb + 8 * i);
+            }
+          }
+        }
+        if (mine && !finite) prompt_row_again<E, D>(p, sq, row, h, visible, m == kNegInf ? 0.f : m, rl);
+      }
+    } else if (mine) {
+      Piece<E, 8> z;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z.w[i] = 0;
+      for (int d = 0; d < D; d += 8) z.store(dst + d);
+    }
+    if (mine && ok && p.lse)
+      p.lse[h * p.lse_stride + sq.q0 + row] = visible > 0 ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && tid == 0) atomicExch(p.err, 1);
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace sage

@@ -297,9 +297,190 @@ SAGE_API sage_status sage_fp8_quant_rows(const void* x, int R, int K, int64_t ld
 SAGE_API sage_status sage_fp8_linear(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw,
                                      int M, int N, int K, void* out, int out_fp32, sage_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving calls: rotary positions, a quantized paged KV cache, and causal
+ * attention over packed prompts and over the cache - what a conditioner in
+ * front of the blocks above needs to read a prompt and go on token by token.
+ *
+ * They share the conventions above, except that:
+ *  - rows are [T, H, D] with a token stride in elements (0 means H*D; at least
+ *    H*D, a multiple of 8), heads contiguous, in one of sage_dtype;
+ *  - counts of zero tokens or sequences are allowed: nothing is launched;
+ *  - slots, pages and lengths live on the device.  A kernel never reads or
+ *    writes outside the cache: it skips an index that is out of range and
+ *    records it, and sage_check() then returns SAGE_ERR_INVALID_ARG once.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { SAGE_BF16 = 0, SAGE_FP16 = 1, SAGE_FP32 = 2 } sage_dtype;
+
+/* Token rows of a call; in == out (and equal strides) works in place. */
+typedef struct {
+  const void* in;
+  void* out;
+  int H;               /* 0: absent                                          */
+  int64_t in_stride;   /* elements between tokens; 0 means H*D               */
+  int64_t out_stride;
+} sage_rows;
+
+/* Rotation per position of every channel pair.  Filled by
+ * sage_rope_plan_init(); `turns`, `axis` and `mscale` may be changed after. */
+#define SAGE_ROPE_MAX_PAIRS 128
+#define SAGE_ROPE_MAX_AXES 8
+typedef struct {
+  int rot_dim;         /* channels that turn, even, 2 .. 256; the rest pass   */
+  int interleaved;     /* pair i: channels (2i, 2i+1), else (i, i + rot_dim/2) */
+  int n_axes;          /* position axes, 1 .. SAGE_ROPE_MAX_AXES              */
+  float mscale;        /* factor on cos and sin                              */
+  double turns[SAGE_ROPE_MAX_PAIRS];         /* revolutions per position      */
+  unsigned char axis[SAGE_ROPE_MAX_PAIRS];   /* position axis of the pair     */
+} sage_rope_plan;
+
+/* f_i = base^(-2i/rot_dim) radians per position, for a context `factor` times
+ * longer than orig_len:
+ *  NONE    f_i
+ *  LINEAR  f_i / factor
+ *  NTK     f_i with base * factor^(rot_dim / (rot_dim - 2))
+ *  YARN    g f_i + (1 - g) f_i / factor, g = clamp((n_i - beta_slow) /
+ *          (beta_fast - beta_slow), 0, 1), n_i = orig_len f_i / (2 pi) the
+ *          revolutions over the original context; mscale = 0.1 ln(factor) + 1 */
+typedef enum {
+  SAGE_ROPE_NONE = 0,
+  SAGE_ROPE_LINEAR = 1,
+  SAGE_ROPE_NTK = 2,
+  SAGE_ROPE_YARN = 3
+} sage_rope_scaling;
+
+/* axis: position axis of each of the rot_dim/2 pairs, or NULL (all 0).  Host
+ * only.  base > 1 and factor >= 1, finite; YARN also needs orig_len >= 1 and
+ * beta_fast > beta_slow > 0. */
+SAGE_API sage_status sage_rope_plan_init(sage_rope_plan* plan, int rot_dim, int interleaved, double base,
+                                         int scaling, double factor, int orig_len, double beta_fast,
+                                         double beta_slow, const unsigned char* axis);
+
+/*
+ * sage_rope - rotary positions of Q and K in one launch.
+ *
+ * in : q, k       rows of T tokens, type `dtype` (either may be absent).
+ *      positions  int64 [n_axes, T], 8-byte aligned; any sign.
+ *      transpose  0: the rotation; non-zero: its transpose, i.e. the gradient
+ *                 of the rotation (its inverse where mscale is 1).
+ * out: with theta = positions[axis_i] * turns_i revolutions, c = mscale cos
+ *      theta, s = mscale sin theta, pair (a, b) -> (a c - b s, a s + b c),
+ *      computed in 32 bits and rounded once; the other channels are copied
+ *      (left alone in place).  The angle is reduced to a fraction of a
+ *      revolution in binary64, so positions far out keep their angle.
+ * D a multiple of 8 up to 256, rot_dim <= D.  Rows of `in` and `out` overlap
+ * either fully (in place) or not at all.
+ */
+SAGE_API sage_status sage_rope(sage_rows q, sage_rows k, int T, int D, int dtype, const int64_t* positions,
+                               const sage_rope_plan* plan, int transpose, sage_stream_t stream);
+
+/* A quantized KV cache in pages.  Codes [num_pages, Hk, page_size, D], one byte
+ * each; scales f32 [num_pages, Hk, page_size], one per token and KV head.  The
+ * slot of a token is page * page_size + offset. */
+typedef enum { SAGE_KV_INT8 = 0, SAGE_KV_E4M3 = 1 } sage_kv_format;
+typedef struct {
+  void* k_codes;
+  float* k_scale;
+  void* v_codes;
+  float* v_scale;
+  int num_pages;
+  int page_size;       /* a power of two, 16 .. 1024                         */
+  int Hk;              /* KV heads                                           */
+  int D;               /* 64 or 128                                          */
+  int format;          /* sage_kv_format                                     */
+} sage_kv_cache;
+
+/*
+ * sage_kv_write - quantize T token rows of K and V into their cache slots.
+ *
+ * in : k, v   [T, Hk, D] of `dtype`, token strides k_stride, v_stride.
+ *      slots  int64 [T]; a negative slot's row is not written.  The slots of a
+ *             call are distinct; rows that name one slot twice leave one of
+ *             them, or a mix of the two, there.
+ * Rule per row of D channels (that of SAGE_GRAN_TOKEN and sage_fp8_quant_rows):
+ * top = 127 (INT8) or 448 (E4M3), amax = max|x|, scale = RN(amax / top), code =
+ * RNE(RN(x * RN(top / amax))); rows with amax < 2^-100 get scale 0 and zero
+ * codes; rows with an infinity or NaN get scale NaN and zero codes, so they read
+ * back as NaN.  Slots that are not named keep their contents.
+ */
+SAGE_API sage_status sage_kv_write(const void* k, const void* v, int T, int64_t k_stride, int64_t v_stride,
+                                   int dtype, const int64_t* slots, sage_kv_cache cache, sage_stream_t stream);
+
+/*
+ * sage_kv_read - the rows of T cache slots, dequantized: RN_dtype(RN(code *
+ * scale)) into k, v [T, Hk, D].  Rows of negative slots are left as they were.
+ * A slot may be named more than once.
+ */
+SAGE_API sage_status sage_kv_read(sage_kv_cache cache, const int64_t* slots, int T, void* k, void* v,
+                                  int64_t k_stride, int64_t v_stride, int dtype, sage_stream_t stream);
+
+/*
+ * sage_attn_prompt - attention over packed sequences of different lengths with
+ * grouped heads, on 16-bit Q, K, V.
+ *
+ * in : q [Tq, Hq, D], k, v [Tk, Hk, D] (BF16 or FP16, token strides), Hq a
+ *      multiple of Hk, D 64 or 128.  cu_q, cu_k: HOST offsets of n_seq + 1
+ *      entries (start at 0, do not decrease); cu_k NULL: the same as cu_q.
+ *      Tq = cu_q[n_seq], Tk = cu_k[n_seq].
+ *      causal: query i of a sequence sees key j when j <= i + Lk - Lq (the ends
+ *      are aligned: the queries are the last Lq of Lk tokens); 0: every key.
+ *      sm_scale <= 0 selects 1/sqrt(D).
+ * out: out [Tq, Hq, D] of the same type; lse f32 [Hq, Tq], the natural log of
+ *      the softmax denominator, or NULL.  A query that sees no key gets zeros
+ *      and -inf.  Keys it does not see do not reach it, whatever they hold.
+ * Scores, sums and output accumulate in 32 bits; the weights are rounded to the
+ * operands' type for the second product.
+ */
+typedef struct {
+  int n_seq;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int Hq, Hk, D;
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  int dtype;
+  int causal;
+  float sm_scale;
+} sage_prompt;
+
+SAGE_API sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const sage_prompt* p, void* out,
+                                      float* lse, sage_stream_t stream);
+
+/*
+ * sage_attn_token - attention of one query token per sequence over the cache.
+ *
+ * in : q [B, Hq, D] BF16 or FP16 (q_stride between sequences), Hq a multiple of
+ *      the cache's Hk.  page_table int32 [B, table_stride]: entry i is the page
+ *      of tokens i * page_size ..; lens int32 [B]: keys 0 .. lens[b] - 1 are
+ *      seen (0 or less: none).  Only the first ceil(lens[b] / page_size) entries
+ *      of a row are read.  max_len: an upper bound on lens, at most
+ *      table_stride * page_size (longer lens are cut there and recorded); it
+ *      sets the launch and the workspace.  sm_scale <= 0 selects 1/sqrt(D).
+ * out: out [B, Hq, D] of q's type; lse f32 [B, Hq] or NULL; zeros and -inf for a
+ *      sequence without keys.  A page outside the cache is left out and
+ *      recorded.
+ * workspace: sage_attn_token_workspace_bytes() bytes, 256-byte aligned; calls
+ * on one stream may share it, graphs that run at the same time may not.
+ */
+typedef struct {
+  int B, Hq;
+  int64_t q_stride, out_stride;
+  int dtype;
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* lens;
+  int max_len;
+  float sm_scale;
+} sage_token;
+
+SAGE_API size_t sage_attn_token_workspace_bytes(int B, int Hq, int Hk, int D, int max_len);
+SAGE_API sage_status sage_attn_token(const void* q, const sage_token* p, sage_kv_cache cache, void* out, float* lse,
+                                     void* workspace, size_t ws_bytes, sage_stream_t stream);
+
 /* Synchronises `stream`, then reports and clears a device-side wait timeout
- * raised by any kernel of this library (SAGE_ERR_DEVICE_TIMEOUT), or a CUDA
- * error (SAGE_ERR_CUDA); SAGE_OK otherwise. */
+ * raised by any kernel of this library (SAGE_ERR_DEVICE_TIMEOUT), a slot or page
+ * index outside a KV cache (SAGE_ERR_INVALID_ARG), or a CUDA error
+ * (SAGE_ERR_CUDA); SAGE_OK otherwise. */
 SAGE_API sage_status sage_check(sage_stream_t stream);
 
 /* Bound, in nanoseconds, on every wait inside the library's kernels (default

@@ -1,0 +1,140 @@
+"""sage_attn_prompt against plain attention in 64 bits (tests/serve_ref.py states the bound)."""
+import math
+
+import pytest
+import torch
+
+from tests.serve_ref import attend, check
+
+pytestmark = pytest.mark.gpu
+
+
+def _offsets(lens):
+    out = [0]
+    for n in lens:
+        out.append(out[-1] + n)
+    return out
+
+
+def _inputs(lq, lk, Hq, Hk, D, dtype, seed=0, pad=8):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    Tq, Tk = sum(lq), sum(lk)
+    q = (1.5 * torch.randn(Tq, Hq * D + pad, generator=g, device="cuda")).to(dtype)[:, : Hq * D].view(Tq, Hq, D)
+    kv = torch.randn(Tk, 2 * Hk * D + pad, generator=g, device="cuda").to(dtype)
+    return q, kv[:, : Hk * D].view(Tk, Hk, D), kv[:, Hk * D: 2 * Hk * D].view(Tk, Hk, D)
+
+
+def _compare(out, lse, q, k, v, cq, ck, causal, scale=None, heads=None):
+    Hq, D = q.shape[1], q.shape[2]
+    G = Hq // k.shape[1]
+    scale = D ** -0.5 if scale is None else scale
+    for s in range(len(cq) - 1):
+        a, b, c, d = cq[s], cq[s + 1], ck[s], ck[s + 1]
+        if a == b:
+            continue
+        n = torch.arange(b - a, device="cuda") + 1 + (d - c) - (b - a)
+        vis = n.clamp(0, d - c) if causal else torch.full_like(n, d - c)
+        for h in (range(Hq) if heads is None else heads):
+            ref = attend(q[a:b, h].double(), k[c:d, h // G].double(), v[c:d, h // G].double(), vis, scale,
+                         torch.finfo(q.dtype).eps / 2)
+            check(out[a:b, h], lse[h, a:b], *ref, what=(s, h))
+
+
+CASES = [
+    # lq, lk, Hq, Hk, D, causal
+    ([1], [1], 1, 1, 64, True),
+    ([1], [300], 4, 2, 128, True),
+    ([128], [128], 2, 1, 128, True),
+    ([256], [256], 2, 2, 64, True),
+    ([129], [129], 3, 1, 128, True),
+    ([257, 1, 127], [257, 1, 127], 4, 1, 64, True),
+    ([77, 130, 1, 333, 64, 19, 256, 100], None, 4, 2, 128, True),
+    ([100, 40, 0, 200], [1000, 40, 77, 333], 2, 1, 128, True),      # continued prompts, an empty one
+    ([300, 129], [7, 128], 2, 1, 64, True),                        # fewer keys than queries: rows without any
+    ([200, 50], [0, 60], 2, 2, 128, True),                         # no keys at all
+    ([300], [500], 2, 2, 128, False),
+    ([50, 200], [1, 129], 6, 2, 64, False),
+    ([1500], [1500], 7, 1, 128, True),
+    ([900], [2600], 2, 1, 64, True),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lq,lk,Hq,Hk,D,causal", CASES)
+def test_prompt(adt, dtype, lq, lk, Hq, Hk, D, causal):
+    lk = lq if lk is None else lk
+    q, k, v = _inputs(lq, lk, Hq, Hk, D, dtype, seed=sum(lq) + D)
+    cq, ck = _offsets(lq), _offsets(lk)
+    out = torch.full((sum(lq), Hq, D), 9.0, device="cuda").to(dtype)
+    lse = torch.full((Hq, sum(lq)), 9.0, device="cuda")
+    adt.sage_attn_prompt(q, k, v, cq, ck, out, lse, causal=causal)
+    adt.sage_check()
+    _compare(out, lse, q, k, v, cq, ck, causal)
+    again = torch.empty_like(out)
+    adt.sage_attn_prompt(q, k, v, cq, torch.tensor(ck, dtype=torch.int32), again, causal=causal)
+    assert torch.equal(out, again)
+
+
+def test_scale_and_large_scores(adt):
+    """Scores that grow along the row move the reference often; an own sm_scale."""
+    L, D = 700, 128
+    q, k, v = _inputs([L], [L], 2, 1, D, torch.bfloat16, seed=4)
+    k = (k.float() * torch.linspace(0.05, 6, L, device="cuda")[:, None, None]).bfloat16()
+    lse = torch.empty(2, L, device="cuda")
+    out = adt.sage_attn_prompt(q, k, v, [0, L], lse=lse, sm_scale=0.2)
+    _compare(out, lse, q, k, v, [0, L], [0, L], True, scale=0.2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_what_masked_places_hold_does_not_matter(adt, dtype):
+    """Infinities and NaN in the K and V of later tokens and of the next sequence."""
+    L, D = 200, 64
+    q, k, v = _inputs([L, 90], [L, 90], 2, 1, D, dtype, seed=6)
+    clean = adt.sage_attn_prompt(q, k, v, [0, L, L + 90])
+    q2, k2, v2 = q.clone(), k.clone(), v.clone()
+    k2[L:], v2[L:] = float("nan"), float("inf")                     # the next sequence
+    k2[150:L], v2[150:L] = float("inf"), float("nan")               # later tokens of the first
+    v2[149, :, 5] = float("-inf")                                   # one channel of one token
+    got = adt.sage_attn_prompt(q2, k2, v2, [0, L, L + 90])
+    adt.sage_check()
+    lim = 2 * torch.finfo(dtype).eps * clean[:149].double().abs() + 4 * torch.finfo(dtype).eps
+    assert bool(((got[:149].double() - clean[:149].double()).abs() <= lim).all())
+    assert bool(torch.isinf(got[149, :, 5]).all()) and bool(torch.isfinite(got[149, :, :5]).all())
+    assert bool(torch.isnan(got[150:L]).all())
+
+
+def test_more_sequences_than_one_launch(adt):
+    lens = [(7 * i) % 23 for i in range(300)]
+    cu = _offsets(lens)
+    q, k, v = _inputs(lens, lens, 2, 1, 64, torch.float16, seed=9)
+    lse = torch.empty(2, cu[-1], device="cuda")
+    out = adt.sage_attn_prompt(q, k, v, cu, lse=lse)
+    _compare(out, lse, q, k, v, cu, cu, True)
+
+
+def test_no_sequences(adt):
+    e = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for cu in ([0], [0, 0, 0]):
+        assert adt.sage_attn_prompt(e, e, e, cu).shape == (0, 2, 64)
+
+
+def test_graph_and_side_stream(adt):
+    L, D = 500, 128
+    q, k, v = _inputs([L], [L], 4, 2, D, torch.bfloat16, seed=11)
+    want = adt.sage_attn_prompt(q, k, v, [0, L])
+    out = torch.zeros_like(want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    adt.sage_attn_prompt(q, k, v, [0, L], out=out, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want)
+    out.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        adt.sage_attn_prompt(q, k, v, [0, L], out=out)
+    q.mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    adt.sage_check()
+    assert torch.equal(out, adt.sage_attn_prompt(q, k, v, [0, L]))
+    assert not math.isclose(float((out.float() - want.float()).abs().max()), 0.0)
