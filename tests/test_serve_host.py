@@ -1,0 +1,247 @@
+"""The serving calls on the host (no GPU needed): every refusal comes before any CUDA call, with its status and a
+message; the Python layer checks layouts that the C ABI cannot see."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+FAKE = 0x10000   # aligned, never dereferenced
+
+
+def _gpu():
+    return torch.cuda.is_available()
+
+
+def _plan(adt, rot=64, **kw):
+    return adt.RopePlan(rot, **kw)
+
+
+def test_plan_refusals(adt):
+    for kw in (dict(rot_dim=0), dict(rot_dim=7), dict(rot_dim=258), dict(rot_dim=64, base=1.0),
+               dict(rot_dim=64, base=float("nan")), dict(rot_dim=64, base=float("inf")),
+               dict(rot_dim=64, scaling="linear", factor=0.5), dict(rot_dim=64, scaling="ntk", factor=float("inf")),
+               dict(rot_dim=64, scaling="yarn", factor=2.0, orig_len=0),
+               dict(rot_dim=64, scaling="yarn", factor=2.0, orig_len=10, beta_fast=1.0, beta_slow=1.0),
+               dict(rot_dim=64, scaling="yarn", factor=2.0, orig_len=10, beta_slow=0.0),
+               dict(rot_dim=4, axis=[0, 8])):
+        with pytest.raises(adt.SageError) as e:
+            adt.RopePlan(**kw)
+        assert e.value.status == 1 and len(str(e.value)) > 30
+    for kw in (dict(scaling="other"), dict(axis=[0]), dict(inv_freq=[1.0])):
+        with pytest.raises(ValueError):
+            adt.RopePlan(64, **kw)
+    assert adt._lib.sage_rope_plan_init(None, 64, 0, 10000.0, 0, 1.0, 0, 32.0, 1.0, None) == 1
+    bad = adt.SageRopePlan()
+    assert adt._lib.sage_rope_plan_init(ctypes.byref(bad), 64, 0, 10000.0, 9, 1.0, 0, 32.0, 1.0, None) == 1
+
+
+def test_plan_formulas(adt):
+    r, base, s, L0 = 96, 10000.0, 8.0, 4096
+    want = [base ** (-2 * i / r) for i in range(r // 2)]
+    turns = lambda p: [t * 2 * math.pi for t in p.struct.turns[: r // 2]]  # noqa: E731
+    assert turns(_plan(adt, r)) == pytest.approx(want, rel=1e-14)
+    assert turns(_plan(adt, r, scaling="linear", factor=s)) == pytest.approx([f / s for f in want], rel=1e-14)
+    b2 = base * s ** (r / (r - 2))
+    assert turns(_plan(adt, r, scaling="ntk", factor=s)) == pytest.approx([b2 ** (-2 * i / r) for i in range(r // 2)],
+                                                                           rel=1e-13)
+    p = _plan(adt, r, scaling="yarn", factor=s, orig_len=L0, beta_fast=20, beta_slow=2)
+    ramp = [min(1, max(0, (L0 * f / (2 * math.pi) - 2) / 18)) for f in want]
+    assert turns(p) == pytest.approx([g * f + (1 - g) * f / s for g, f in zip(ramp, want)], rel=1e-13)
+    assert 0 in ramp and 1 in ramp and any(0 < g < 1 for g in ramp)
+    assert p.struct.mscale == pytest.approx(0.1 * math.log(s) + 1, rel=1e-6)
+    # the last pair of an NTK plan turns `factor` times slower, the first as before
+    ntk = turns(_plan(adt, r, scaling="ntk", factor=s))
+    assert ntk[0] == pytest.approx(want[0]) and ntk[-1] == pytest.approx(want[-1] / s, rel=1e-12)
+    assert _plan(adt, 2, scaling="ntk", factor=s).struct.turns[0] * 2 * math.pi == pytest.approx(1.0)
+    axes = _plan(adt, 8, axis=[0, 2, 1, 2])
+    assert axes.n_axes == 3 and list(axes.struct.axis[:4]) == [0, 2, 1, 2]
+    assert _plan(adt, 8, mscale=0.5).struct.mscale == 0.5
+
+
+def test_rope_refusals(adt):
+    L = adt._lib
+    plan = _plan(adt, 64)
+
+    def call(q=(FAKE, FAKE, 4, 0, 0), k=(FAKE, FAKE, 2, 0, 0), T=3, D=64, dt=0, pos=FAKE, pl=plan.struct):
+        return L.sage_rope(adt.SageRows(*q), adt.SageRows(*k), T, D, dt, pos, None if pl is None else ctypes.byref(pl),
+                           0, None)
+
+    assert call(pl=None) == 1
+    assert call(T=-1) == 1
+    assert call(D=60) == 2 and call(D=264) == 2 and call(D=0) == 2
+    assert call(dt=3) == 1
+    assert call(D=56) == 1                                    # rot_dim above D
+    assert call(q=(FAKE, FAKE, -1, 0, 0)) == 1
+    assert call(q=(None, FAKE, 4, 0, 0)) == 1 and call(k=(FAKE, None, 2, 0, 0)) == 1
+    assert call(q=(FAKE + 8, FAKE, 4, 0, 0)) == 3
+    assert call(q=(FAKE, FAKE, 4, 255, 0)) == 1 and call(q=(FAKE, FAKE, 4, 260, 0)) == 3
+    assert call(q=(FAKE, FAKE, 4, 512, 256)) == 1             # in place with two strides
+    assert call(pos=None) == 1 and call(pos=FAKE + 4) == 3
+    for field, value in (("rot_dim", 63), ("n_axes", 0), ("n_axes", 9)):
+        bad = adt.SageRopePlan.from_buffer_copy(plan.struct)
+        setattr(bad, field, value)
+        assert call(pl=bad) == 1, field
+    bad = adt.SageRopePlan.from_buffer_copy(plan.struct)
+    bad.axis[5] = 1
+    assert call(pl=bad) == 1 and b"axis" in L.sage_last_error()
+    bad = adt.SageRopePlan.from_buffer_copy(plan.struct)
+    bad.turns[0] = float("nan")
+    assert call(pl=bad) == 1
+    assert call(T=0, q=(None, None, 4, 0, 0), k=(None, None, 2, 0, 0), pos=None) == 0
+    assert call(q=(None, None, 0, 0, 0), k=(None, None, 0, 0, 0)) == 0
+    if not _gpu():
+        assert call() == 4
+
+
+def _cache(adt, **over):
+    a = dict(k_codes=FAKE, k_scale=FAKE, v_codes=FAKE, v_scale=FAKE, num_pages=4, page_size=16, Hk=2, D=64, format=0)
+    a.update(over)
+    return adt.SageKvCache(*[a[f] for f, _ in adt.SageKvCache._fields_])
+
+
+BAD_CACHES = [(dict(num_pages=0), 1), (dict(Hk=0), 1), (dict(page_size=8), 2), (dict(page_size=24), 2),
+              (dict(page_size=2048), 2), (dict(D=96), 2), (dict(format=2), 1), (dict(k_codes=None), 1),
+              (dict(v_scale=None), 1), (dict(v_codes=FAKE + 8), 3), (dict(k_scale=FAKE + 4), 3)]
+
+
+@pytest.mark.parametrize("over,status", BAD_CACHES)
+def test_cache_refusals(adt, over, status):
+    L, c = adt._lib, _cache(adt, **over)
+    assert L.sage_kv_write(FAKE, FAKE, 3, 0, 0, 0, FAKE, c, None) == status
+    assert L.sage_kv_read(c, FAKE, 3, FAKE, FAKE, 0, 0, 0, None) == status
+    p = adt.SageToken(1, 4, 0, 0, 0, FAKE, 4, FAKE, 64, 0.0)
+    assert L.sage_attn_token(FAKE, ctypes.byref(p), c, FAKE, None, FAKE << 8, 1 << 30, None) == status
+
+
+def test_write_and_read_refusals(adt):
+    L, c = adt._lib, _cache(adt)
+
+    def both(status, k=FAKE, v=FAKE, T=3, ks=0, vs=0, dt=0, slots=FAKE, c=c):
+        assert L.sage_kv_write(k, v, T, ks, vs, dt, slots, c, None) == status
+        assert L.sage_kv_read(c, slots, T, k, v, ks, vs, dt, None) == status
+
+    both(1, T=-1)
+    both(1, dt=7)
+    both(1, k=None)
+    both(3, v=FAKE + 2)
+    both(1, slots=None)
+    both(3, slots=FAKE + 4)
+    both(1, ks=64)
+    both(3, vs=129)
+    both(1, T=(1 << 31) - 1)
+    both(0, T=0, k=None, v=None, slots=None)
+    if not _gpu():
+        both(4)
+
+
+def _prompt(adt, cu_q, cu_k=None, **over):
+    a = dict(Hq=4, Hk=2, D=64, q_stride=0, k_stride=0, v_stride=0, out_stride=0, dtype=0, causal=1, sm_scale=0.0)
+    a.update(over)
+    arrs = [None if c is None else (ctypes.c_int32 * len(c))(*c) for c in (cu_q, cu_k)]
+    p = adt.SagePrompt(a.pop("n_seq", len(cu_q) - 1 if cu_q else 1), *[None if x is None else ctypes.addressof(x) for x in arrs],
+                       a["Hq"], a["Hk"], a["D"], a["q_stride"], a["k_stride"], a["v_stride"], a["out_stride"],
+                       a["dtype"], a["causal"], a["sm_scale"])
+    p._keep = arrs
+    return p
+
+
+def test_prompt_refusals(adt):
+    L = adt._lib
+
+    def call(p, q=FAKE, k=FAKE, v=FAKE, out=FAKE, lse=None):
+        return L.sage_attn_prompt(q, k, v, None if p is None else ctypes.byref(p), out, lse, None)
+
+    ok = [0, 3, 10]
+    assert call(None) == 1
+    assert call(_prompt(adt, ok, n_seq=-1)) == 1
+    assert call(_prompt(adt, None)) == 1
+    for cu in ([1, 3], [0, 5, 3]):
+        assert call(_prompt(adt, cu)) == 1 and call(_prompt(adt, [0] * len(cu), cu)) == 1
+    assert call(_prompt(adt, ok, Hq=3)) == 1 and call(_prompt(adt, ok, Hk=0)) == 1 and call(_prompt(adt, ok, Hq=0)) == 1
+    assert call(_prompt(adt, ok, D=96)) == 2
+    assert call(_prompt(adt, ok, dtype=2)) == 2
+    for s in (float("nan"), float("inf"), float("-inf")):
+        assert call(_prompt(adt, ok, sm_scale=s)) == 1
+    for name in ("q_stride", "out_stride"):
+        assert call(_prompt(adt, ok, **{name: 128})) == 1 and call(_prompt(adt, ok, **{name: 260})) == 3
+    for name in ("k_stride", "v_stride"):
+        assert call(_prompt(adt, ok, **{name: 64})) == 1 and call(_prompt(adt, ok, **{name: 132})) == 3
+    for name in ("q", "k", "v", "out"):
+        assert call(_prompt(adt, ok), **{name: None}) == 1 and call(_prompt(adt, ok), **{name: FAKE + 2}) == 3
+    assert call(_prompt(adt, ok), lse=FAKE + 2) == 3
+    assert call(_prompt(adt, [0]), q=None) == 0 and call(_prompt(adt, [0, 0], [0, 7]), q=None) == 0
+    if not _gpu():
+        assert call(_prompt(adt, ok)) == 4
+        assert call(_prompt(adt, ok, [0, 0, 0]), k=None, v=None) == 4      # no keys: K and V are not needed
+
+
+def test_token_refusals(adt):
+    L, c = adt._lib, _cache(adt)
+
+    def call(q=FAKE, out=FAKE, lse=None, ws=FAKE << 8, wsb=1 << 30, c=c, null=False, **over):
+        a = dict(B=2, Hq=4, q_stride=0, out_stride=0, dtype=0, page_table=FAKE, table_stride=40, lens=FAKE, max_len=640,
+                 sm_scale=0.0)
+        a.update(over)
+        p = adt.SageToken(*[a[f] for f, _ in adt.SageToken._fields_])
+        return L.sage_attn_token(q, None if null else ctypes.byref(p), c, out, lse, ws, wsb, None)
+
+    assert call(null=True) == 1
+    assert call(Hq=3) == 1 and call(Hq=0) == 1
+    assert call(B=-1) == 1 and call(B=70000) == 1
+    assert call(dtype=2) == 2
+    assert call(sm_scale=float("nan")) == 1
+    assert call(q_stride=128) == 1 and call(out_stride=257) == 3
+    assert call(max_len=641) == 1 and call(max_len=-1) == 1 and call(table_stride=-1) == 1
+    assert call(q=None) == 1 and call(out=FAKE + 8) == 3
+    assert call(lens=None) == 1 and call(page_table=None) == 1
+    assert call(lens=FAKE + 2) == 3 and call(page_table=FAKE + 1) == 3 and call(lse=FAKE + 2) == 3
+    need = adt.attn_token_workspace_bytes(2, 4, 2, 64, 640)
+    assert need > 0 and need % 256 == 0
+    assert call(ws=None) == 6 and call(ws=(FAKE << 8) + 16) == 3 and call(wsb=need - 1) == 6
+    assert call(B=0, q=None, lens=None, page_table=None, ws=None) == 0
+    assert call(c=_cache(adt, Hk=40000), Hq=40000 * 17) == 1                # too many heads
+    if not _gpu():
+        assert call(wsb=need) == 4
+        assert call(max_len=0, page_table=None, ws=None) == 4               # no keys at all
+    assert adt.attn_token_workspace_bytes(2, 3, 2, 64, 640) == 0            # Hq no multiple of Hk
+    assert adt.attn_token_workspace_bytes(2, 4, 2, 96, 640) == 0
+    assert adt.attn_token_workspace_bytes(0, 4, 2, 64, 640) == 0
+
+
+def test_python_layer_refuses_layouts(adt):
+    """Layouts are checked before the device: these tensors are on the CPU or meta, and each call names its fault."""
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    slots = torch.zeros(3, dtype=torch.int64)
+    cache = adt.KVCache(2, 16, 2, 64, device="cpu")
+    with pytest.raises(ValueError, match="CUDA device"):
+        adt.sage_rope(x, x, slots, adt.RopePlan(64))
+    with pytest.raises(ValueError, match="CUDA device"):
+        cache.write(x, x, slots)
+    with pytest.raises(ValueError, match="CUDA device"):
+        adt.sage_attn_prompt(x, x, x, [0, 3])
+    with pytest.raises(ValueError, match="fmt"):
+        adt.KVCache(2, 16, 2, 64, fmt="int4", device="cpu")
+    with pytest.raises(ValueError, match="strides"):
+        adt._row_stride("q", torch.zeros(3, 64, 2).transpose(1, 2), 2, 64)
+    with pytest.raises(ValueError, match="must be"):
+        adt._row_stride("q", x, 2, 32)
+    assert adt._row_stride("q", torch.zeros(1, 2, 64)[:, :, :], 2, 64) == 0
+    assert adt._row_stride("q", torch.zeros(3, 5, 64)[:, :2], 2, 64) == 320
+    with pytest.raises(TypeError):
+        adt._row_dtype("x", torch.zeros(1, dtype=torch.float64))
+    with pytest.raises(TypeError):
+        adt._row_dtype("x", x, x.half())
+    with pytest.raises(ValueError, match="end at"):
+        adt._offsets("cu_q", [0, 2], 3)
+    with pytest.raises(ValueError, match="contiguous"):
+        adt._int_vector("slots", torch.zeros(6, dtype=torch.int64)[::2], 3, torch.int64)
+    with pytest.raises(ValueError, match="contiguous"):
+        adt._int_vector("slots", slots.int(), 3, torch.int64)
+    kc, ks, vc, vs = cache.tensors
+    for bad in ((kc.float(), ks, vc, vs), (kc, ks, vc.view(torch.uint8), vs), (kc, ks.double(), vc, vs)):
+        with pytest.raises(TypeError):
+            adt._cache("x", *bad)
+    for bad in ((kc, ks[:1], vc, vs), (kc.transpose(0, 1), ks, vc, vs), (kc[0], ks, vc[0], vs)):
+        with pytest.raises(ValueError):
+            adt._cache("x", *bad)
