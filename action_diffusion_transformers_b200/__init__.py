@@ -15,8 +15,9 @@ and so do the serving calls beside them:
 
 This module only marshals arguments: torch tensors provide device memory and
 the current CUDA stream; every step of the computation runs in the library's
-CUDA kernels.  Importing it loads libsage.so and raises ImportError if the
-library has not been built (there is no fallback implementation).
+CUDA kernels.  Importing it loads libsage.so, and the extension module that
+hands tensors to the serving calls, and raises ImportError if they have not been
+built (there is no fallback implementation).
 """
 from __future__ import annotations
 
@@ -32,6 +33,7 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libsage.so is not built ({LIB_PATH}); run "
                       "`python -m action_diffusion_transformers_b200.build`")
 _lib = ctypes.CDLL(LIB_PATH)
+from . import _serve_ext  # noqa: E402  (built beside the library)
 
 SAGE_OK = 0
 STATUS_NAMES = {0: "SAGE_OK", 1: "SAGE_ERR_INVALID_ARG", 2: "SAGE_ERR_UNSUPPORTED", 3: "SAGE_ERR_ALIGNMENT",
@@ -61,8 +63,6 @@ class SageNormRope(ctypes.Structure):
 
 ROPE_MAX_PAIRS = 128
 ROPE_SCALING = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}   # sage_rope_scaling
-DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}           # sage_dtype
-KV_FORMAT = {torch.int8: 0, torch.float8_e4m3fn: 1, torch.uint8: 1}        # sage_kv_format, by the codes' type
 
 
 class SageRows(ctypes.Structure):
@@ -299,53 +299,6 @@ def selftest_wait_timeout(timeout_ns: int, stream=None) -> None:
 
 
 # ------------------------------------------------------------------ serving calls
-def _same_device(name, first, *rest):
-    """The one CUDA device of a call's tensors (None among them is skipped)."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: tensors must be on a CUDA device (got {dev})")
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-    return dev
-
-
-def _row_stride(name, t, H, D):
-    """Token stride of rows [T, H, D] whose heads are contiguous (0 where there is one row at most)."""
-    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D:
-        raise ValueError(f"{name} must be [T, {H}, {D}] (got {tuple(t.shape)})")
-    st = t.stride()
-    if t.numel() and (st[2] != 1 or (H > 1 and st[1] != D)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous (strides {st})")
-    return st[0] if t.shape[0] > 1 else 0
-
-
-def _row_dtype(name, t, *rest):
-    code = DTYPE.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name}: dtype {t.dtype} is not one of {list(DTYPE)}")
-    for r in rest:
-        if r is not None and r.dtype != t.dtype:
-            raise TypeError(f"{name}: {r.dtype} beside {t.dtype}")
-    return code
-
-
-def _int_vector(name, t, n, dtype):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{n}] (got {t.dtype} {tuple(t.shape)})")
-
-
-def _launch(dev, stream, call, where):
-    """Runs call(stream pointer) with the tensors' device current, on the given stream or that device's current one."""
-    if dev.index == torch.cuda.current_device():
-        status = call(torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream))
-    else:
-        with torch.cuda.device(dev):
-            status = call(_stream(stream))
-    if status != SAGE_OK:
-        raise SageError(status, where)
-
-
 class RopePlan:
     """Rotation per position of every channel pair (sage_rope_plan).
 
@@ -372,7 +325,7 @@ class RopePlan:
                 self.struct.turns[i] = float(f) / 6.283185307179586
         if mscale is not None:
             self.struct.mscale = float(mscale)
-        self._ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
     n_axes = property(lambda self: self.struct.n_axes)
     rot_dim = property(lambda self: self.struct.rot_dim)
@@ -381,110 +334,41 @@ class RopePlan:
 def sage_rope(q, k, positions, plan, q_out=None, k_out=None, transpose=False, stream=None):
     """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (either may be None) in one launch.  positions: int64 [T], or
     [axes, T].  In place without q_out / k_out.  transpose: the gradient of the rotation.  Returns (q_out, k_out)."""
-    x = q if q is not None else k
     q_out = q if q_out is None else q_out
     k_out = k if k_out is None else k_out
-    dev = _same_device("sage_rope", x, k, q_out, k_out, positions)
-    dt = _row_dtype("sage_rope", x, k, q_out, k_out)
-    T, D = x.shape[0], x.shape[2] if x.dim() == 3 else 0
-    rows = []
-    for name, a, b in (("q", q, q_out), ("k", k, k_out)):
-        if a is None:
-            rows.append(SageRows(None, None, 0, 0, 0))
-            continue
-        if a.dim() != 3 or a.shape[0] != T or b.shape != a.shape:
-            raise ValueError(f"{name} and {name}_out must be [{T}, H, {D}] (got {tuple(a.shape)}, {tuple(b.shape)})")
-        H = a.shape[1]
-        rows.append(SageRows(a.data_ptr(), b.data_ptr(), H, _row_stride(name, a, H, D), _row_stride(name + "_out", b, H, D)))
-    n = plan.struct.n_axes
-    if positions.dtype != torch.int64 or positions.numel() != n * T or positions.shape[-1] != T \
-            or not positions.is_contiguous():
-        raise ValueError(f"positions must be contiguous int64 [{T}] or [{n}, {T}] (got {positions.dtype} "
-                         f"{tuple(positions.shape)})")
-    _launch(dev, stream, lambda st: _lib.sage_rope(rows[0], rows[1], T, D, dt, positions.data_ptr(), plan._ref,
-                                                   int(bool(transpose)), st), "sage_rope")
+    status = _serve_ext.rope(q, k, positions, plan.address, q_out, k_out, transpose, stream)
+    if status:
+        raise SageError(status, "sage_rope")
     return q_out, k_out
 
 
-def _cache(name, k_codes, k_scale, v_codes, v_scale):
-    """sage_kv_cache of codes [pages, Hk, page_size, D] (int8, or float8_e4m3fn / uint8) and float32 scales
-    [pages, Hk, page_size]."""
-    fmt = KV_FORMAT.get(k_codes.dtype)
-    if fmt is None or v_codes.dtype != k_codes.dtype:
-        raise TypeError(f"{name}: codes must both be int8, float8_e4m3fn or uint8 (got {k_codes.dtype}, {v_codes.dtype})")
-    shape = k_codes.shape
-    if len(shape) != 4 or v_codes.shape != shape or k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
-        raise ValueError(f"{name}: codes must be [pages, Hk, page_size, D] and scales [pages, Hk, page_size] (got "
-                         f"{tuple(shape)}, {tuple(v_codes.shape)}, {tuple(k_scale.shape)}, {tuple(v_scale.shape)})")
-    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
-        raise TypeError(f"{name}: scales must be float32")
-    if not (k_codes.is_contiguous() and v_codes.is_contiguous() and k_scale.is_contiguous()
-            and v_scale.is_contiguous()):
-        raise ValueError(f"{name}: the cache must be contiguous")
-    return SageKvCache(k_codes.data_ptr(), k_scale.data_ptr(), v_codes.data_ptr(), v_scale.data_ptr(), shape[0],
-                       shape[2], shape[1], shape[3], fmt)
-
-
-def _kv_rows(name, k, v, slots, c):
-    T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError(f"{name}: k and v have {T} and {v.shape[0]} rows")
-    _int_vector(f"{name}: slots", slots, T, torch.int64)
-    return T, _row_stride("k", k, c.Hk, c.D), _row_stride("v", v, c.Hk, c.D), _row_dtype(name, k, v)
-
-
+# The cache of the calls below: codes [pages, Hk, page_size, D] (int8, or float8_e4m3fn / uint8 for E4M3) and float32
+# scales [pages, Hk, page_size], of K and of V.
 def sage_kv_write(k, v, slots, k_codes, k_scale, v_codes, v_scale, stream=None):
     """Quantizes the rows of k, v [T, Hk, D] into the cache slots (int64 [T]; page * page_size + offset; a negative
     slot's row is not written)."""
-    dev = _same_device("sage_kv_write", k, v, slots, k_codes, k_scale, v_codes, v_scale)
-    c = _cache("sage_kv_write", k_codes, k_scale, v_codes, v_scale)
-    T, ks, vs, dt = _kv_rows("sage_kv_write", k, v, slots, c)
-    _launch(dev, stream, lambda st: _lib.sage_kv_write(k.data_ptr(), v.data_ptr(), T, ks, vs, dt, slots.data_ptr(), c,
-                                                       st), "sage_kv_write")
+    status = _serve_ext.kv_write(k, v, slots, k_codes, k_scale, v_codes, v_scale, stream)
+    if status:
+        raise SageError(status, "sage_kv_write")
 
 
 def sage_kv_read(slots, k_codes, k_scale, v_codes, v_scale, k, v, stream=None):
     """Dequantizes the cache slots (int64 [T]) into k, v [T, Hk, D]; rows of negative slots keep their contents."""
-    dev = _same_device("sage_kv_read", k, v, slots, k_codes, k_scale, v_codes, v_scale)
-    c = _cache("sage_kv_read", k_codes, k_scale, v_codes, v_scale)
-    T, ks, vs, dt = _kv_rows("sage_kv_read", k, v, slots, c)
-    _launch(dev, stream, lambda st: _lib.sage_kv_read(c, slots.data_ptr(), T, k.data_ptr(), v.data_ptr(), ks, vs, dt,
-                                                      st), "sage_kv_read")
+    status = _serve_ext.kv_read(k, v, slots, k_codes, k_scale, v_codes, v_scale, stream)
+    if status:
+        raise SageError(status, "sage_kv_read")
     return k, v
 
 
-def _offsets(name, cu, total):
-    if isinstance(cu, torch.Tensor):
-        if cu.is_cuda:
-            raise ValueError(f"{name} must be on the host (a list or a CPU tensor)")
-        cu = cu.tolist()
-    if len(cu) < 1 or cu[-1] != total:
-        raise ValueError(f"{name} must end at the {total} packed rows (got {list(cu)[-1:]})")
-    return (ctypes.c_int32 * len(cu))(*cu)
-
-
 def sage_attn_prompt(q, k, v, cu_q, cu_k=None, out=None, lse=None, causal=True, sm_scale=0.0, stream=None):
-    """Attention over packed sequences: q [Tq, Hq, D], k, v [Tk, Hk, D] BF16 or FP16; cu_q, cu_k host offsets (cu_k None:
-    cu_q).  causal: query i of a sequence sees keys j <= i + Lk - Lq.  lse: float32 [Hq, Tq] or None.  Returns out."""
-    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
-    dev = _same_device("sage_attn_prompt", q, k, v, out, lse)
-    dt = _row_dtype("sage_attn_prompt", q, k, v, out)
-    if q.dim() != 3 or k.dim() != 3 or out.shape != q.shape or k.shape != v.shape:
-        raise ValueError(f"sage_attn_prompt: q, out [Tq, Hq, D] and k, v [Tk, Hk, D] are wanted (got {tuple(q.shape)}, "
-                         f"{tuple(out.shape)}, {tuple(k.shape)}, {tuple(v.shape)})")
-    Tq, Hq, D = q.shape
-    Hk = k.shape[1]
-    cq = _offsets("cu_q", cu_q, Tq)
-    ck = _offsets("cu_k", cu_q if cu_k is None else cu_k, k.shape[0])
-    if len(ck) != len(cq):
-        raise ValueError(f"cu_q and cu_k name {len(cq) - 1} and {len(ck) - 1} sequences")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (Hq, Tq) or not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous float32 [{Hq}, {Tq}]")
-    p = SagePrompt(len(cq) - 1, ctypes.addressof(cq), ctypes.addressof(ck), Hq, Hk, D, _row_stride("q", q, Hq, D),
-                   _row_stride("k", k, Hk, D), _row_stride("v", v, Hk, D), _row_stride("out", out, Hq, D), dt,
-                   int(bool(causal)), float(sm_scale))
-    _launch(dev, stream, lambda st: _lib.sage_attn_prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(p),
-                                                          out.data_ptr(), _ptr(lse), st), "sage_attn_prompt")
+    """Attention over packed sequences: q [Tq, Hq, D], k, v [Tk, Hk, D] BF16 or FP16; cu_q, cu_k host offsets, a list or a
+    CPU tensor (cu_k None: cu_q).  causal: query i of a sequence sees keys j <= i + Lk - Lq.  lse: float32 [Hq, Tq] or
+    None.  Returns out."""
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    status = _serve_ext.attn_prompt(q, k, v, cu_q, cu_k, out, lse, causal, sm_scale, stream)
+    if status:
+        raise SageError(status, "sage_attn_prompt")
     return out
 
 
@@ -497,31 +381,10 @@ def sage_attn_token(q, k_codes, k_scale, v_codes, v_scale, page_table, lens, out
     """Attention of one token per sequence, q [B, Hq, D] BF16 or FP16, over the cache: page_table int32 [B, pages],
     lens int32 [B] (keys seen).  max_len: upper bound on lens (None: what the table can name).  workspace: at least
     attn_token_workspace_bytes(...) bytes, kept by the caller.  lse: float32 [B, Hq] or None.  Returns out."""
-    dev = _same_device("sage_attn_token", q, k_codes, k_scale, v_codes, v_scale, page_table, lens, out, workspace, lse)
-    c = _cache("sage_attn_token", k_codes, k_scale, v_codes, v_scale)
-    dt = _row_dtype("sage_attn_token", q, out)
-    if q.dim() != 3 or out.shape != q.shape:
-        raise ValueError(f"sage_attn_token: q and out must be [B, Hq, D] (got {tuple(q.shape)}, {tuple(out.shape)})")
-    B, Hq, D = q.shape
-    if D != c.D:
-        raise ValueError(f"sage_attn_token: q has D = {D}, the cache {c.D}")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B \
-            or (page_table.numel() and page_table.stride(1) != 1):
-        raise ValueError(f"page_table must be int32 [{B}, pages], rows contiguous (got {page_table.dtype} "
-                         f"{tuple(page_table.shape)})")
-    _int_vector("lens", lens, B, torch.int32)
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, Hq) or not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous float32 [{B}, {Hq}]")
-    pages = page_table.shape[1]
-    if max_len is None:
-        max_len = pages * c.page_size
-    elif max_len > pages * c.page_size:
-        raise ValueError(f"max_len {max_len} is above what the page table can name ({pages * c.page_size})")
-    p = SageToken(B, Hq, _row_stride("q", q, Hq, D), _row_stride("out", out, Hq, D), dt, page_table.data_ptr(),
-                  page_table.stride(0) if B > 1 else pages, lens.data_ptr(), max_len, float(sm_scale))
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _launch(dev, stream, lambda st: _lib.sage_attn_token(q.data_ptr(), ctypes.byref(p), c, out.data_ptr(), _ptr(lse),
-                                                         _ptr(workspace), ws_bytes, st), "sage_attn_token")
+    status = _serve_ext.attn_token(q, k_codes, k_scale, v_codes, v_scale, page_table, lens, out, workspace, max_len, lse,
+                                   sm_scale, stream)
+    if status:
+        raise SageError(status, "sage_attn_token")
     return out
 
 

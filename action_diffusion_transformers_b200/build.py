@@ -1,4 +1,5 @@
-"""Build the CUDA library libsage.so in-tree for sm_100a (B200).
+"""Build the CUDA library libsage.so, and the extension module that hands torch
+tensors to its serving calls, in-tree for sm_100a (B200).
 
     python -m action_diffusion_transformers_b200.build [--verbose]
 
@@ -7,7 +8,8 @@ csrc/serve_api.cu (rotary positions, KV cache, prompt and single-token
 attention), each with the kernel headers it includes, side by side and links
 them into a shared library with the CUDA runtime linked statically, so the .so
 loads on a machine without a GPU (for the symbol checks) and on the B200 machine
-alongside torch.
+alongside torch.  g++ compiles csrc/serve_ext.cpp against the installed torch's
+headers into _serve_ext.so, which is linked to libsage.so beside it.
 """
 from __future__ import annotations
 
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +25,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsage.so")
+EXT = os.path.join(PKG, "_serve_ext.so")
+EXT_SOURCE = os.path.join(CSRC, "serve_ext.cpp")
 SOURCES = [os.path.join(CSRC, "sage_api.cu"), os.path.join(CSRC, "serve_api.cu")]
 
 
@@ -31,7 +36,7 @@ def deps() -> list:
     out = []
     for d in (CSRC, INCLUDE):
         for name in sorted(os.listdir(d)):
-            if name.endswith((".cu", ".cuh", ".h")):
+            if name.endswith((".cu", ".cuh", ".h", ".cpp")):
                 out.append(os.path.join(d, name))
     return out
 
@@ -43,10 +48,23 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def ext_command(out: str) -> list:
+    """g++ command of the extension module.  It leaves the torch libraries to be
+    found where `import torch` has loaded them, and libsage.so beside itself."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+            + [f for d in inc for f in ("-isystem", d)] + [EXT_SOURCE, "-o", out, "-L", os.path.join(root, "lib")]
+            + ["-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-L", PKG, "-l:libsage.so", "-Wl,-rpath,$ORIGIN"])
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return all(os.path.getmtime(d) <= t for d in deps())
 
 
@@ -71,6 +89,11 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
     os.replace(LIB + ".tmp", LIB)
+    cmd = ext_command(EXT + ".tmp")
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+    os.replace(EXT + ".tmp", EXT)
     return LIB
 
 

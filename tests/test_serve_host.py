@@ -210,38 +210,92 @@ def test_token_refusals(adt):
 
 
 def test_python_layer_refuses_layouts(adt):
-    """Layouts are checked before the device: these tensors are on the CPU or meta, and each call names its fault."""
+    """Layouts are checked before the device: these tensors are on the CPU, and each call names its fault."""
     x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
     slots = torch.zeros(3, dtype=torch.int64)
+    plan = adt.RopePlan(64)
     cache = adt.KVCache(2, 16, 2, 64, device="cpu")
-    with pytest.raises(ValueError, match="CUDA device"):
-        adt.sage_rope(x, x, slots, adt.RopePlan(64))
-    with pytest.raises(ValueError, match="CUDA device"):
-        cache.write(x, x, slots)
-    with pytest.raises(ValueError, match="CUDA device"):
-        adt.sage_attn_prompt(x, x, x, [0, 3])
+    kc, ks, vc, vs = cache.tensors
+    table, lens = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
     with pytest.raises(ValueError, match="fmt"):
         adt.KVCache(2, 16, 2, 64, fmt="int4", device="cpu")
-    with pytest.raises(ValueError, match="strides"):
-        adt._row_stride("q", torch.zeros(3, 64, 2).transpose(1, 2), 2, 64)
-    with pytest.raises(ValueError, match="must be"):
-        adt._row_stride("q", x, 2, 32)
-    assert adt._row_stride("q", torch.zeros(1, 2, 64)[:, :, :], 2, 64) == 0
-    assert adt._row_stride("q", torch.zeros(3, 5, 64)[:, :2], 2, 64) == 320
-    with pytest.raises(TypeError):
-        adt._row_dtype("x", torch.zeros(1, dtype=torch.float64))
-    with pytest.raises(TypeError):
-        adt._row_dtype("x", x, x.half())
-    with pytest.raises(ValueError, match="end at"):
-        adt._offsets("cu_q", [0, 2], 3)
+
+    def rope(q=x, k=x, pos=slots, **kw):
+        adt.sage_rope(q, k, pos, plan, **kw)
+
+    def write(k=x, v=x, sl=slots, c=(kc, ks, vc, vs)):
+        adt.sage_kv_write(k, v, sl, *c)
+
+    def read(k=x, v=x, sl=slots, c=(kc, ks, vc, vs)):
+        adt.sage_kv_read(sl, *c, k, v)
+
+    def prompt(q=x, k=x, v=x, cu=(0, 3), **kw):
+        adt.sage_attn_prompt(q, k, v, cu, **kw)
+
+    def token(q=x, c=(kc, ks, vc, vs), t=table, ln=lens, out=x, ws=None, **kw):
+        adt.sage_attn_token(q, *c, t, ln, out, ws, **kw)
+
+    for call in (rope, write, read, prompt, token):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+    wide, narrow = torch.zeros(3, 64, 2, dtype=torch.bfloat16).transpose(1, 2), torch.zeros(3, 2, 32, dtype=torch.bfloat16)
+    for bad, kind, word in ((wide, ValueError, "strides"), (narrow, ValueError, "must be"), (x[0], ValueError, "must be"),
+                            (x[:1].expand(3, 2, 64), ValueError, "stride 0"), (x.double(), TypeError, "dtype|beside|Double"),
+                            (7, TypeError, "tensor")):
+        for call in (rope, write, read, prompt):
+            with pytest.raises(kind, match=word if not (call is rope and bad is narrow) else "must be"):
+                call(k=bad)
+    for call in (write, read, prompt):
+        with pytest.raises(TypeError, match="beside"):
+            call(v=x.half())
+    with pytest.raises(ValueError, match="q or k"):
+        rope(q=None, k=None)
+    with pytest.raises(ValueError, match="q_out"):
+        rope(q_out=narrow)
+    with pytest.raises(ValueError, match="positions"):
+        rope(pos=slots.int())
+    with pytest.raises(ValueError, match="positions"):
+        rope(pos=slots[:2])
+    with pytest.raises(ValueError, match="positions"):
+        rope(pos=torch.zeros(2, 3, dtype=torch.int64))
+    for call in (write, read):
+        for bad in (torch.zeros(6, dtype=torch.int64)[::2], slots.int(), slots[:2]):
+            with pytest.raises(ValueError, match="slots"):
+                call(sl=bad)
+    for call in (write, read, token):
+        for bad in ((kc.float(), ks, vc, vs), (kc, ks, vc.view(torch.uint8), vs), (kc, ks.double(), vc, vs)):
+            with pytest.raises(TypeError):
+                call(c=bad)
+        for bad in ((kc, ks[:1], vc, vs), (kc.transpose(0, 1), ks, vc, vs), (kc[0], ks, vc[0], vs)):
+            with pytest.raises(ValueError):
+                call(c=bad)
     with pytest.raises(ValueError, match="contiguous"):
-        adt._int_vector("slots", torch.zeros(6, dtype=torch.int64)[::2], 3, torch.int64)
-    with pytest.raises(ValueError, match="contiguous"):
-        adt._int_vector("slots", slots.int(), 3, torch.int64)
-    kc, ks, vc, vs = cache.tensors
-    for bad in ((kc.float(), ks, vc, vs), (kc, ks, vc.view(torch.uint8), vs), (kc, ks.double(), vc, vs)):
-        with pytest.raises(TypeError):
-            adt._cache("x", *bad)
-    for bad in ((kc, ks[:1], vc, vs), (kc.transpose(0, 1), ks, vc, vs), (kc[0], ks, vc[0], vs)):
-        with pytest.raises(ValueError):
-            adt._cache("x", *bad)
+        write(c=(torch.zeros(2, 2, 32, 64, dtype=torch.int8)[:, :, ::2], ks, vc, vs))
+    for bad in ((0, 2), [], [0, 1, 2], torch.tensor([0, 2])):
+        with pytest.raises(ValueError, match="cu_q"):
+            prompt(cu=bad)
+    with pytest.raises(ValueError, match="cu_q"):
+        prompt(cu=[0, -1, 3])
+    with pytest.raises(ValueError, match="sequences"):
+        prompt(cu_k=[0, 1, 3])
+    with pytest.raises(TypeError):
+        prompt(cu=5)
+    for bad in (torch.zeros(3, 2), torch.zeros(2, 3, dtype=torch.float64), torch.zeros(3, 2).t()):
+        with pytest.raises(ValueError, match="lse"):
+            prompt(lse=bad)
+    with pytest.raises(ValueError, match="out"):
+        prompt(out=narrow)
+    for bad in (table.long(), table[:2], table.t(), table[:1].expand(3, 2)):
+        with pytest.raises(ValueError, match="page_table"):
+            token(t=bad)
+    with pytest.raises(ValueError, match="lens"):
+        token(ln=lens.long())
+    for bad in (33, -1):
+        with pytest.raises(ValueError, match="max_len"):
+            token(max_len=bad)
+    with pytest.raises(ValueError, match="lse"):
+        token(lse=torch.zeros(2, 3))
+    with pytest.raises(ValueError, match="workspace"):
+        token(ws=torch.zeros(64)[::2])
+    with pytest.raises(ValueError, match="q must be|out must be"):
+        token(q=narrow)
