@@ -7,18 +7,23 @@
 // row, their bounds given by the host.
 //
 // One CTA takes 256 query rows (two tiles of 128, A and B) of one (sequence,
-// head), 320 threads:
+// head), 384 threads:
 //   warps 0-3, 4-7  softmax of tile A, of tile B: thread r owns query row r
 //                   (TMEM lane r), reads its 128 scores, writes P back as
-//                   16-bit pairs over the first 64 score columns, rescales its
-//                   row of O when the reference m moves, and stores the row.
-//   warp 8          MMA: S = Q K^T (shared x shared), O += P V (P in TMEM).
-//   warp 9          TMA loads: Q once, K and V tiles of 128 keys into a ring.
-// TMEM (512 columns): S_A, S_B at 0, 128; O_A, O_B at 256, 384.
+//                   16-bit pairs over the first 64 score columns, 64 keys at a
+//                   time, rescales its row of O when the reference m moves, and
+//                   stores the row.
+//   warps 8, 9      MMA of tile A, of tile B: S = Q K^T (shared x shared),
+//                   O += P V (P in TMEM).
+//   warp 10         TMA loads: Q once, K and V tiles of 128 keys into a ring.
+// TMEM (512 columns): S_A, S_B at 0, 128; O_A, O_B at 256, 384 (D = 128: P lies
+// over the first half of S) or 256, 320 with P_A, P_B at 384, 448 (D = 64).
 // While tile A's softmax runs, the tensor core works on tile B and the other
-// way round.  S_X(j+1) overwrites the columns that PV_X(j) reads P from, so it
-// is issued only after PV_X(j) has completed; a softmax thread that sees
-// S_X(j) therefore knows that O_X holds every product up to j - 1.
+// way round.  D = 128: S_X(j+1) overwrites the columns that PV_X(j) reads P
+// from, so it is issued only after PV_X(j) has completed, and a softmax thread
+// that sees S_X(j) knows that O_X holds every product up to j - 1.  D = 64:
+// S_X(j+1) is issued as soon as the softmax has read S_X(j), and P_X(j) is
+// written once PV_X(j-1) has completed.
 //
 // The reference m of a row moves only when a score passes it by 2^8 (P stays
 // below 2^8 in 16 bits and the sums in 32 bits), so O is rescaled rarely.  P is
@@ -40,7 +45,8 @@
 namespace sage {
 
 constexpr int kPrTile = 128;
-constexpr int kPrThreads = 320;
+constexpr int kPrThreads = 384;          // 2 x 4 softmax warps, two for MMA, one for loads, one idle
+constexpr int kPrWarpMma = 8, kPrWarpLoad = 10;
 constexpr int kPrMaxSeq = 256;          // sequences per launch
 constexpr float kPrRaise = 8.f;
 
@@ -51,9 +57,11 @@ struct PrSmem {
   static constexpr int kQ = 0;                                // A, B
   static constexpr int kRing = 2 * kTileBytes;
   static constexpr int kBar = kRing + kSlots * kTileBytes;
-  // q[2], s_full[2], p_full[2], pv_done[2], full[], empty[], drain
-  static constexpr int kQFull = 0, kSFull = 2, kPFull = 4, kPVDone = 6, kFull = 8, kEmpty = 8 + kSlots,
-                       kDrain = 8 + 2 * kSlots, kNumBars = 9 + 2 * kSlots;
+  static constexpr bool kApart = D == 64;                     // P has TMEM columns of its own
+  static constexpr int kColO = 256, kStepO = D, kColP = kApart ? 384 : 0, kStepP = kApart ? 64 : 128;
+  // q[2], s_full[2], pv_done[2], p_full[2][2], s_read[2], full[], empty[], drain[2]
+  static constexpr int kQFull = 0, kSFull = 2, kPVDone = 4, kPFull = 6, kSRead = 10, kFull = 12,
+                       kEmpty = kFull + kSlots, kDrain = kEmpty + kSlots, kNumBars = kDrain + 2;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kTotal = kMisc + 16;
   static constexpr int kAlloc = kTotal + 1024;
@@ -105,14 +113,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 // Descriptor of an operand whose rows (128-byte swizzled, 8-row groups of 1024
 // bytes) run along the product's K axis and whose 64-element row pieces lie
 // `piece` bytes apart (V: keys are rows, channels are contiguous).
@@ -126,13 +126,77 @@ __device__ __forceinline__ uint64_t make_sdesc_mn(uint32_t saddr, uint32_t piece
   return d;
 }
 
+// 2^x on the FMA and integer pipes, for the share of the weights that would
+// queue at the special-function unit (16 results a clock per SM): x = n + f with
+// n = round(x), 2^f by a polynomial with minimax relative error on [-1/2, 1/2]
+// (fitted by linear programming), n added to the exponent field.  Cubic (1.0e-4)
+// where the weights are rounded to bf16 (2^-9), quartic (2.8e-6) for fp16
+// (2^-12).  Two pairs of each 16: on 8192 tokens x 32 heads, D = 128 / 64, none
+// takes 574 / 501 us, two 558 / 480, four 558 / 479, six 557 / 487, eight (an
+// earlier kernel) 691: the FMA pipe, at 3 cycles a packed operation, fills up.
+constexpr int kPrPolyOf16 = 2;
+__host__ __device__ constexpr bool pr_on_fma(int i) { return (i * kPrPolyOf16) % 16 < kPrPolyOf16; }
+template <bool kCubic>
+__device__ __forceinline__ f32x2_t pr_exp2_poly(f32x2_t x) {
+  x = x2_pack(__float_as_uint(fmaxf(x2_lo(x), kExp2Min)), __float_as_uint(fmaxf(x2_hi(x), kExp2Min)));
+  const f32x2_t round = x2_splat(kExp2Round);
+  const f32x2_t xr = x2_add(x, round);
+  const f32x2_t f = x2_sub(x, x2_sub(xr, round));
+  f32x2_t p;
+  if constexpr (kCubic) {
+    p = x2_fma(x2_splat(0.055009059607982635f), f, x2_splat(0.2422109693288803f));
+    p = x2_fma(p, f, x2_splat(0.6932829022407532f));
+  } else {
+    p = x2_fma(x2_splat(0.009582576341927052f), f, x2_splat(0.05590682849287987f));
+    p = x2_fma(p, f, x2_splat(0.24024106562137604f));
+    p = x2_fma(p, f, x2_splat(0.6931241154670715f));
+  }
+  p = x2_fma(p, f, x2_splat(1.f));
+  return x2_add_exponent(p, xr);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// The weights of 64 keys, added up and written in 16-bit pairs to 32 TMEM
+// columns.  kMasked: scores of -inf weigh nothing, exactly (the polynomial never
+// gives less than 2^-126, so it takes no part there).
+template <class E, bool kMasked>
+__device__ __forceinline__ void pr_weights(const uint32_t (&s0)[32], const uint32_t (&s1)[32], f32x2_t sl2,
+                                           f32x2_t nref2, uint32_t col, f32x2_t (&sum)[4]) {
+  constexpr bool kBf16 = std::is_same<E, Bf16T>::value;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t(&s)[32] = c == 0 ? s0 : s1;
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const f32x2_t t = x2_fma(x2_pack(s[2 * i], s[2 * i + 1]), sl2, nref2);
+      f32x2_t w;
+      if (!kMasked && pr_on_fma(i))
+        w = pr_exp2_poly<kBf16>(t);
+      else
+        w = x2_pack(__float_as_uint(ex2_approx(x2_lo(t))), __float_as_uint(ex2_approx(x2_hi(t))));
+      sum[i & 3] = x2_add(sum[i & 3], w);
+      pk[i] = E::pack(x2_lo(w), x2_hi(w));
+    }
+    tmem_st16(col + 16 * c, pk);
+  }
+}
+
 // A softmax warp stays whole in front of its warp-wide TMEM accesses.
 __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int64_t tmo) {
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, tmo));
 }
 
-// One row once more from its visible keys, channel by channel group, in 32
-// bits: only for rows whose first result was not finite.
+// One row once more from its visible keys, 8 channels at a time, in 32 bits:
+// only for rows whose first result was not finite.
 template <class E, int D>
 __device__ __noinline__ void prompt_row_again(const PromptParams& p, const PromptSeq& sq, int row, int h, int visible,
                                               float m, float rl) {
@@ -170,6 +234,19 @@ __device__ __noinline__ void prompt_row_again(const PromptParams& p, const Promp
     r.put(o);
     r.store(out + d);
   }
+}
+
+// The launch gives each of the 384 threads 168 registers; the last four warps
+// hand most of theirs to the softmax warps: 2 x 224 + 56 = 3 x 168.
+constexpr int kPrRegsSoftmax = 224, kPrRegsOther = 56;
+static_assert(2 * kPrRegsSoftmax + kPrRegsOther <= 3 * 168, "register split");
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 template <class E, int D>
@@ -213,13 +290,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   }
   const int n = max(nt[0], nt[1]);
 
-  if (warp == 8) {
+  if (warp == kPrWarpMma) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i)
-      mbar_init(&bars[i], i == L::kPFull || i == L::kPFull + 1 ? kPrTile : 1);
+      // P, S read: one arrival per softmax warp; a ring slot is empty when both tiles have read it
+      mbar_init(&bars[i], i >= L::kPFull && i < L::kFull ? 4 : i >= L::kEmpty && i < L::kDrain ? 2 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -228,7 +306,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 9) {
+  bool again = false;                      // this thread's row has to be computed once more
+  float again_m = 0.f, again_rl = 0.f;
+  int again_row = 0, again_visible = 0;
+  if (warp >= kPrWarpMma) {
+   regs_dec<kPrRegsOther>();
+   if (warp == kPrWarpLoad) {
     // ------------------------------------------------------------ loads
     if (lane == 0 && n > 0) {
       tma_prefetch_desc(&tm_q);
@@ -265,9 +348,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
       }
     }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ MMA
+   } else if (warp < kPrWarpLoad) {
+    // ------------------------------------------------------------ MMA of tile A, of tile B
     if (lane == 0 && n > 0) {
+      const int x = warp - kPrWarpMma;
       constexpr uint32_t kFmt = kBf16 ? 1u : 0u;
       constexpr uint32_t kIdescQK = make_idesc(1u, kFmt, 128u, 128u);
       constexpr uint32_t kIdescPV = make_idesc(1u, kFmt, 128u, static_cast<uint32_t>(D)) | (1u << 16);
@@ -276,7 +360,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       };
       auto slot_of = [&](int it) { return it % kSlots; };
       auto wait_full = [&](int it) { return wait(L::kFull + slot_of(it), it / kSlots); };
-      auto scores = [&](int x, int j) {           // S_x(j) = Q_x K_j^T
+      auto scores = [&](int j) {                  // S_x(j) = Q_x K_j^T
         const uint64_t qd = make_sdesc(smem_u32(smem + L::kQ + x * L::kTileBytes), 1024u, 2u);
         const uint64_t kd = make_sdesc(smem_u32(smem + L::kRing + slot_of(2 * j) * L::kTileBytes), 1024u, 2u);
 #pragma unroll
@@ -286,57 +370,70 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         tc_commit(&bars[L::kSFull + x]);
       };
-      auto products = [&](int x, int j) {         // O_x += P_x(j) V_j
+      auto products = [&](int j) {                // O_x += P_x(j) V_j, as its halves come in
         const uint64_t vd =
             make_sdesc_mn(smem_u32(smem + L::kRing + slot_of(2 * j + 1) * L::kTileBytes), kPrTile * 128);
 #pragma unroll
-        for (int kk = 0; kk < kPrTile / 16; ++kk)
-          mma_f16_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, vd + kk * (16 * 128 / 16), kIdescPV,
-                     (j > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(&bars[L::kPVDone + x]);
-      };
-      bool ok = wait_full(0);
-      for (int x = 0; x < 2 && ok; ++x)
-        if (nt[x] > 0) {
-          ok = wait(L::kQFull + x, 0);
-          if (ok) {
-            tc_fence_after();
-            scores(x, 0);
-          }
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(L::kPFull + 2 * x + half, j)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+            mma_f16_ts(tmem + L::kColO + x * L::kStepO, tmem + L::kColP + x * L::kStepP + kk * 8, vd + kk * (16 * 128 / 16), kIdescPV,
+                       (j > 0 || kk > 0) ? 1u : 0u);
         }
+        tc_commit(&bars[L::kPVDone + x]);
+        return true;
+      };
+      // A commit arrives when all that this thread issued before has completed
+      // (at once for a tile without work), so each slot is given back by both.
+      bool ok = wait_full(0) && (nt[x] == 0 || wait(L::kQFull + x, 0));
+      if (ok && nt[x] > 0) {
+        tc_fence_after();
+        scores(0);
+      }
       if (ok) tc_commit(&bars[L::kEmpty + slot_of(0)]);
       for (int j = 0; ok && j < n; ++j) {
-        if (!(ok = wait_full(2 * j + 1))) break;
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (j < nt[x]) {
-            if (!(ok = wait(L::kPFull + x, j))) break;
-            tc_fence_after();
-            products(x, j);
+        if constexpr (L::kApart) {
+          if (j + 1 < n) {
+            if (!(ok = wait_full(2 * j + 2) && (j + 1 >= nt[x] || wait(L::kSRead + x, j)))) break;
             if (j + 1 < nt[x]) {
-              // S_x(j+1) takes the columns that hold P_x(j): wait for its products.
-              if (!(ok = wait_full(2 * j + 2) && wait(L::kPVDone + x, j))) break;
               tc_fence_after();
-              scores(x, j + 1);
+              scores(j + 1);
             }
+            tc_commit(&bars[L::kEmpty + slot_of(2 * j + 2)]);
+          }
+          if (!(ok = wait_full(2 * j + 1) && (j >= nt[x] || products(j)))) break;
+          tc_commit(&bars[L::kEmpty + slot_of(2 * j + 1)]);
+        } else {
+          if (!(ok = wait_full(2 * j + 1) && (j >= nt[x] || products(j)))) break;
+          tc_commit(&bars[L::kEmpty + slot_of(2 * j + 1)]);
+          if (j + 1 < n) {
+            // S_x(j+1) takes the columns that hold P_x(j): wait for its products.
+            if (!(ok = wait_full(2 * j + 2) && (j + 1 >= nt[x] || wait(L::kPVDone + x, j)))) break;
+            if (j + 1 < nt[x]) {
+              tc_fence_after();
+              scores(j + 1);
+            }
+            tc_commit(&bars[L::kEmpty + slot_of(2 * j + 2)]);
           }
         }
-        if (!ok) break;
-        // Completes when all that was issued so far has, so V_j and K_j+1 are read.
-        tc_commit(&bars[L::kEmpty + slot_of(2 * j + 1)]);
-        if (j + 1 < n) tc_commit(&bars[L::kEmpty + slot_of(2 * j + 2)]);
       }
-      tc_commit(&bars[L::kDrain]);
+      tc_commit(&bars[L::kDrain + x]);
       int none = 0;
-      mbar_wait_bounded(&bars[L::kDrain], 0, reinterpret_cast<volatile int*>(&none), 200000000);
+      mbar_wait_bounded(&bars[L::kDrain + x], 0, reinterpret_cast<volatile int*>(&none), 200000000);
     }
+   }
   } else {
     // ------------------------------------------------------------ softmax
+    regs_inc<kPrRegsSoftmax>();
     const int x = warp >> 2;                       // tile A, B
     const int r = tid & 127;
     const int row = row0 + x * kPrTile + r;        // of the sequence
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + x * 128 + lane_base;
-    const uint32_t to = tmem + 256 + x * 128 + lane_base;
+    const uint32_t to = tmem + L::kColO + x * L::kStepO + lane_base;
+    const uint32_t tp = tmem + L::kColP + x * L::kStepP + lane_base;
     const float kNegInf = -__int_as_float(0x7F800000);
     const float sl = p.scale_log2;
     const int visible = p.causal ? min(sq.lk, max(0, row + off + 1)) : sq.lk;
@@ -352,8 +449,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < 4; ++c) reg_fence(s[c]);
+      if constexpr (L::kApart) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kSRead + x]);
+      }
       const int valid = visible - j * kPrTile;
-      if (__any_sync(0xFFFFFFFFu, valid < kPrTile)) {
+      const bool masked = __any_sync(0xFFFFFFFFu, valid < kPrTile);
+      if (masked) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -370,6 +473,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
       }
       const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+      if (L::kApart && j > 0) {      // P and O: the products of tile j - 1 are done
+        if (!(ok = pr_wait(&bars[L::kPVDone + x], static_cast<uint32_t>(j - 1) & 1, abort_flag, tmo))) break;
+        tc_fence_after();
+      }
       if (__any_sync(0xFFFFFFFFu, tmax > m + kPrRaise)) {
         const float m1 = fmaxf(m, tmax);
         const float alpha = m == kNegInf ? 0.f : ex2_approx(m - m1);
@@ -377,7 +484,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         m = m1;
         if (j > 0) {
           const f32x2_t a2 = x2_splat(alpha);
-#pragma unroll
+#pragma unroll 1
           for (int cb = 0; cb < D; cb += 32) {
             f32x2_t o[16];
             tmem_ld32_pairs(to + cb, o);
@@ -387,24 +494,21 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
         }
       }
-      const float ref = m == kNegInf ? 0.f : m;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const f32x2_t sl2 = x2_splat(sl), nref2 = x2_splat(m == kNegInf ? 0.f : -m);
+      f32x2_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float a = ex2_approx(fmaf(__uint_as_float(s[c][2 * i]), sl, -ref));
-          const float b = ex2_approx(fmaf(__uint_as_float(s[c][2 * i + 1]), sl, -ref));
-          sum[i & 3] += a + b;
-          pk[i] = E::pack(a, b);
-        }
-        tmem_st16(ts + 16 * c, pk);
+      for (int half = 0; half < 2; ++half) {
+        if (masked)
+          pr_weights<E, true>(s[2 * half], s[2 * half + 1], sl2, nref2, tp + 32 * half, sum);
+        else
+          pr_weights<E, false>(s[2 * half], s[2 * half + 1], sl2, nref2, tp + 32 * half, sum);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[L::kPFull + 2 * x + half]);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&bars[L::kPFull + x]);
+      const f32x2_t sum2 = x2_add(x2_add(sum[0], sum[1]), x2_add(sum[2], sum[3]));
+      l += x2_lo(sum2) + x2_hi(sum2);
     }
     const bool mine = row < sq.lq;
     S* dst = static_cast<S*>(p.out) + static_cast<int64_t>(sq.q0 + row) * p.out_stride + static_cast<int64_t>(h) * D;
@@ -437,26 +541,32 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
           }
         }
-        if (mine && !finite) prompt_row_again<E, D>(p, sq, row, h, visible, m == kNegInf ? 0.f : m, rl);
+        again = mine && !finite;
+        again_m = m == kNegInf ? 0.f : m;
+        again_rl = rl;
+        again_row = row;
+        again_visible = visible;
+        if (mine && p.lse)
+          p.lse[h * p.lse_stride + sq.q0 + row] = visible > 0 ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
       }
     } else if (mine) {
       Piece<E, 8> z;
 #pragma unroll
       for (int i = 0; i < 4; ++i) z.w[i] = 0;
       for (int d = 0; d < D; d += 8) z.store(dst + d);
+      if (p.lse) p.lse[h * p.lse_stride + sq.q0 + row] = kNegInf;
     }
-    if (mine && ok && p.lse)
-      p.lse[h * p.lse_stride + sq.q0 + row] = visible > 0 ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
   }
 
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (*abort_flag && tid == 0) atomicExch(p.err, 1);
-  if (warp == 8) {
+  if (warp == kPrWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (again) prompt_row_again<E, D>(p, sq, again_row, h, again_visible, again_m, again_rl);
 }
 
 }  // namespace sage
