@@ -54,6 +54,7 @@ sage_status check_cache(const sage_kv_cache& c, sage::KvCacheView* v) {
   v->Hk = c.Hk;
   v->page_shift = 0;
   while ((1 << v->page_shift) < c.page_size) ++v->page_shift;
+  v->by_heads = sage::FastDiv(static_cast<uint32_t>(c.Hk));
   return SAGE_OK;
 }
 
@@ -99,41 +100,66 @@ sage_status kv_rows_args(const void* k, const void* v, int T, int64_t k_stride, 
   return SAGE_OK;
 }
 
-// Keys per CTA of the single-token attention, and CTAs per (sequence, block of
-// heads).
-void token_split(int B, int Hk, int G, int max_len, int* chunk, int* chunks) {
-  const int64_t base = static_cast<int64_t>(B) * Hk * ((G + 15) / 16);
-  const int64_t want = std::max<int64_t>(1, 2664 / std::max<int64_t>(1, base));
-  int64_t c = (max_len + want - 1) / want;
-  c = std::min<int64_t>(std::max<int64_t>((c + 63) / 64 * 64, 128), sage::kTokMaxChunk);
-  *chunk = static_cast<int>(c);
-  *chunks = static_cast<int>(std::max<int64_t>(1, (max_len + c - 1) / c));
+// Query heads per CTA of the single-token attention, in blocks of 8.
+int token_nt(int G) { return G > 8 ? 2 : 1; }
+
+// Segments of a sequence.
+int64_t token_segs(int Hk, int G) { return static_cast<int64_t>(Hk) * ((G + 8 * token_nt(G) - 1) / (8 * token_nt(G))); }
+int64_t token_tiles(int max_len) { return (static_cast<int64_t>(max_len) + sage::kTokTile - 1) / sage::kTokTile; }
+// Tiles of a chunk: as many chunks as CTAs are resident (three per SM), a tile
+// per warp at least, 16 per warp at most, so that uneven sequences spread over
+// the SMs.  (8 KV heads, D = 128, E4M3: one sequence of 8192 keys takes 9.9 us
+// with 444 chunks wanted and 13.4 with 1776, three of 2000 to 8000 keys 13.9 and
+// 20.5; 64 of 300 to 8192 keys 110 us with 4 tiles per warp, 103 with 8, 102 with
+// 16.)
+constexpr int kTokWant = 444, kTokPerMax = 16;
+int token_per(int B, int Hk, int G, int max_len) {
+  const int64_t tiles = token_tiles(max_len), w = sage::kTokWarps;
+  const int64_t chunks = std::max<int64_t>(1, kTokWant / std::max<int64_t>(1, B * token_segs(Hk, G)));
+  const int64_t per = (tiles + chunks - 1) / chunks;
+  return static_cast<int>(std::max(w, std::min(kTokPerMax * w, (per + w - 1) / w * w)));
+}
+int token_chunks(int max_len, int per) {
+  return static_cast<int>(std::max<int64_t>(1, (token_tiles(max_len) + per - 1) / per));
 }
 
-size_t token_ws(int B, int Hq, int D, int chunks) {
-  if (chunks <= 1) return 0;
+// Workspace of the single-token attention: the chunks' results.
+struct TokenWs {
+  size_t part_lse, total;
+};
+TokenWs token_ws(int B, int Hq, int D, int chunks) {
+  if (chunks <= 1) return {0, 0};
   const size_t rows = static_cast<size_t>(B) * Hq * chunks;
-  return (rows * D * 4 + 255) / 256 * 256 + (rows * 4 + 255) / 256 * 256;
+  const size_t o = (rows * D * 4 + 255) / 256 * 256;
+  return {o, o + (rows * 4 + 255) / 256 * 256};
 }
 
-// Shared memory limits of the prompt kernels, once per device.
-std::atomic<uint64_t> g_prompt_ready{0};
+// Shared memory limits of the attention kernels, once per device.
+std::atomic<uint64_t> g_attn_ready{0};
 
+template <class K>
+void attr(cudaError_t* e, K kernel, int bytes) {
+  if (*e == cudaSuccess) *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
 template <class E, int D>
-cudaError_t prompt_attr() {
-  return cudaFuncSetAttribute(sage::prompt_attn_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              sage::PrSmem<D>::kAlloc);
+void attn_attr(cudaError_t* e) {
+  attr(e, sage::prompt_attn_kernel<E, D>, sage::PrSmem<D>::kAlloc);
+  attr(e, sage::token_attn_kernel<E, D, 1, sage::kKvInt8>, sage::kTokSmem<D, 1>);
+  attr(e, sage::token_attn_kernel<E, D, 1, sage::kKvE4m3>, sage::kTokSmem<D, 1>);
+  attr(e, sage::token_attn_kernel<E, D, 2, sage::kKvInt8>, sage::kTokSmem<D, 2>);
+  attr(e, sage::token_attn_kernel<E, D, 2, sage::kKvE4m3>, sage::kTokSmem<D, 2>);
 }
 
-sage_status prompt_setup(int dev) {
+sage_status attn_setup(int dev) {
   const uint64_t bit = uint64_t(1) << dev;
-  if (g_prompt_ready.load() & bit) return SAGE_OK;
-  cudaError_t e = prompt_attr<sage::Bf16T, 128>();
-  if (e == cudaSuccess) e = prompt_attr<sage::Bf16T, 64>();
-  if (e == cudaSuccess) e = prompt_attr<sage::Fp16T, 128>();
-  if (e == cudaSuccess) e = prompt_attr<sage::Fp16T, 64>();
-  if (e != cudaSuccess) return sage_host::cuda_fail(e, "prompt attention setup");
-  g_prompt_ready.fetch_or(bit);
+  if (g_attn_ready.load() & bit) return SAGE_OK;
+  cudaError_t e = cudaSuccess;
+  attn_attr<sage::Bf16T, 128>(&e);
+  attn_attr<sage::Bf16T, 64>(&e);
+  attn_attr<sage::Fp16T, 128>(&e);
+  attn_attr<sage::Fp16T, 64>(&e);
+  if (e != cudaSuccess) return sage_host::cuda_fail(e, "attention setup");
+  g_attn_ready.fetch_or(bit);
   return SAGE_OK;
 }
 
@@ -298,13 +324,15 @@ sage_status sage_rope(sage_rows q, sage_rows k, int T, int D, int dtype, const i
   if (T < 4 * sms) {
     parts = std::min((H + hstep - 1) / hstep, std::max(1, 4 * sms / T));
   } else {
-    const int per = (H + hstep - 1) / hstep;            // heads per thread and token
-    p.tokens = std::max(1, std::min({16 / per, T / (4 * sms), 4096 / p.pairs}));
+    p.tokens = std::max(1, std::min({16 * hstep / H, T / (4 * sms), 4096 / p.pairs}));
   }
   p.head_step = (H + parts - 1) / parts;
+  p.pair_stride = (p.pairs + 3) & ~3;
+  p.by_pairs = sage::FastDiv(static_cast<uint32_t>(p.pairs));
+  p.by_heads = sage::FastDiv(static_cast<uint32_t>(p.head_step));
   parts = (H + p.head_step - 1) / p.head_step;
   const dim3 grid((T + p.tokens - 1) / p.tokens, parts);
-  const size_t smem = static_cast<size_t>(p.tokens) * p.pairs * sizeof(float2);
+  const size_t smem = static_cast<size_t>(p.tokens) * p.pair_stride * sizeof(float2);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   with_type(dtype, [&](auto e) {
     using E = decltype(e);
@@ -326,7 +354,7 @@ sage_status sage_kv_write(const void* k, const void* v, int T, int64_t k_stride,
   int* err;
   if ((st = device_setup(&dev, &err)) != SAGE_OK) return st;
   p.err = err + 1;
-  const int64_t per = sage::kKvThreads / (cache.D / 8) * 4;
+  const int64_t per = sage::kKvThreads / (cache.D / sage::kKvPer) * 2;   // rows per CTA
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) * cache.Hk + per - 1) / per), 2);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   with_type(dtype, [&](auto e) {
@@ -351,7 +379,7 @@ sage_status sage_kv_read(sage_kv_cache cache, const int64_t* slots, int T, void*
   int* err;
   if ((st = device_setup(&dev, &err)) != SAGE_OK) return st;
   p.err = err + 1;
-  const int64_t per = sage::kKvThreads / (cache.D / 8) * 4;
+  const int64_t per = sage::kKvThreads / (cache.D / sage::kKvPer) * 2;   // rows per CTA
   const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) * cache.Hk + per - 1) / per), 2);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   with_type(dtype, [&](auto e) {
@@ -401,7 +429,7 @@ sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const 
   int dev;
   int* err;
   if ((st = device_setup(&dev, &err)) != SAGE_OK) return st;
-  if ((st = prompt_setup(dev)) != SAGE_OK) return st;
+  if ((st = attn_setup(dev)) != SAGE_OK) return st;
 
   CUtensorMap tq, tk, tv;
   if ((st = encode_rows(&tq, q, a->dtype, Tq, a->Hq, a->D, p.q_stride)) != SAGE_OK) return st;
@@ -459,10 +487,7 @@ sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const 
 
 size_t sage_attn_token_workspace_bytes(int B, int Hq, int Hk, int D, int max_len) {
   if (B < 0 || max_len < 0 || (D != 64 && D != 128) || check_heads(Hq, Hk) != SAGE_OK) return 0;
-  if (B == 0) return 0;
-  int chunk, chunks;
-  token_split(B, Hk, Hq / Hk, max_len, &chunk, &chunks);
-  return token_ws(B, Hq, D, chunks);
+  return B == 0 ? 0 : token_ws(B, Hq, D, token_chunks(max_len, token_per(B, Hk, Hq / Hk, max_len))).total;
 }
 
 sage_status sage_attn_token(const void* q, const sage_token* a, sage_kv_cache cache, void* out, float* lse,
@@ -492,22 +517,27 @@ sage_status sage_attn_token(const void* q, const sage_token* a, sage_kv_cache ca
        reinterpret_cast<uintptr_t>(lse)) & 3u)
     return fail(SAGE_ERR_ALIGNMENT, "lens, page_table and lse must be 4-byte aligned");
   const int G = a->Hq / cache.Hk;
-  token_split(a->B, cache.Hk, G, a->max_len, &p.chunk, &p.chunks);
-  const size_t need = token_ws(a->B, a->Hq, cache.D, p.chunks);
-  if (need > 0) {
+  p.per = token_per(a->B, cache.Hk, G, a->max_len);
+  p.chunks = token_chunks(a->max_len, p.per);
+  const TokenWs ws = token_ws(a->B, a->Hq, cache.D, p.chunks);
+  if (ws.total > 0) {
     if (!workspace) return fail(SAGE_ERR_WORKSPACE, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
       return fail(SAGE_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
-    if (ws_bytes < need) return fail(SAGE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+    if (ws_bytes < ws.total)
+      return fail(SAGE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, ws.total);
   }
-  const int nt = G > 8 ? 2 : 1;
+  const int nt = token_nt(G);
   p.head_blocks = (G + 8 * nt - 1) / (8 * nt);
-  const int64_t gy = static_cast<int64_t>(cache.Hk) * p.head_blocks;
-  if (gy > 65535 || static_cast<int64_t>(a->B) * a->Hq >= (int64_t(1) << 31))
-    return fail(SAGE_ERR_INVALID_ARG, "too many heads (Hq = %d, B = %d)", a->Hq, a->B);
-  int dev;
+  const int64_t segs = token_segs(cache.Hk, G), tiles = token_tiles(a->max_len);
+  if (segs > 65535 || static_cast<int64_t>(a->B) * a->Hq >= (int64_t(1) << 31) ||
+      a->B * segs * tiles >= (int64_t(1) << 31))
+    return fail(SAGE_ERR_INVALID_ARG, "too much for one call (B = %d, Hq = %d, max_len = %d)", a->B, a->Hq,
+                a->max_len);
+  int dev, sms = 0;
   int* err;
-  if ((st = device_setup(&dev, &err)) != SAGE_OK) return st;
+  if ((st = device_setup(&dev, &err, &sms)) != SAGE_OK) return st;
+  if ((st = attn_setup(dev)) != SAGE_OK) return st;
 
   p.q = q;
   p.out = out;
@@ -519,8 +549,8 @@ sage_status sage_attn_token(const void* q, const sage_token* a, sage_kv_cache ca
   p.table = a->page_table;
   p.lens = a->lens;
   p.part_o = static_cast<float*>(workspace);
-  const size_t rows = static_cast<size_t>(a->B) * a->Hq * p.chunks;
-  p.part_lse = p.chunks > 1 ? p.part_o + (rows * cache.D * 4 + 255) / 256 * 64 : nullptr;
+  p.part_lse = p.chunks > 1 ? p.part_o + ws.part_lse / 4 : nullptr;
+  p.segs = static_cast<int>(segs);
   p.table_stride = a->table_stride;
   p.B = a->B;
   p.Hq = a->Hq;
@@ -531,21 +561,27 @@ sage_status sage_attn_token(const void* q, const sage_token* a, sage_kv_cache ca
   p.max_len = a->max_len;
   p.scale_log2 = scale_log2(a->sm_scale, cache.D);
   p.err = err + 1;
-  const dim3 grid(p.chunks, static_cast<unsigned>(gy), a->B);
+  const dim3 grid(p.chunks, p.segs, a->B);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   with_flag(a->dtype == SAGE_BF16, [&](auto bf) {
     with_flag(cache.D == 128, [&](auto wide) {
-      using E = std::conditional_t<bf.value, sage::Bf16T, sage::Fp16T>;
-      constexpr int D = wide.value ? 128 : 64;
       with_flag(nt == 2, [&](auto two) {
+        using E = std::conditional_t<bf.value, sage::Bf16T, sage::Fp16T>;
+        constexpr int D = wide.value ? 128 : 64, NT = two.value ? 2 : 1;
         with_flag(cache.format == SAGE_KV_E4M3, [&](auto fp8) {
-          pdl_launch(sage::token_attn_kernel<E, D, two.value ? 2 : 1, fp8.value ? sage::kKvE4m3 : sage::kKvInt8>,
-                     grid, sage::kTokThreads, 0, cs, p);
+          constexpr int kFmt = fp8.value ? sage::kKvE4m3 : sage::kKvInt8;
+          pdl_launch(sage::token_attn_kernel<E, D, NT, kFmt>, grid, sage::kTokThreads, sage::kTokSmem<D, NT>, cs, p);
         });
+        if (p.chunks > 1) {
+          // Few rows have many parts each: four warps to a row.
+          const int64_t rows = static_cast<int64_t>(a->B) * a->Hq;
+          with_flag(rows <= 4 * sms, [&](auto few) {
+            constexpr int kWarps = few.value ? 4 : 1, kPer = sage::kJoinThreads / 32 / kWarps;
+            pdl_launch(sage::token_join_kernel<E, D, kWarps>, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)),
+                       sage::kJoinThreads, 0, cs, p);
+          });
+        }
       });
-      if (p.chunks > 1)
-        pdl_launch(sage::token_join_kernel<E, D>, dim3(static_cast<unsigned>(a->B) * a->Hq), sage::kJoinThreads, 0, cs,
-                   p);
     });
   });
   return launch_check("sage_attn_token launch");

@@ -10,12 +10,16 @@
 // have to pass through registers to become f16 anyway.  Both products take the
 // codes as the 16-row operand and the heads as the 8 columns:
 //   S^T [16 keys x 8 heads] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16] P^T.
-// Fragments come straight from global memory, without shared memory: which
-// channel or key a lane's fragment element stands for is free as long as both
-// operands agree, so each lane reads contiguous pieces of a row:
-//   K: lane (g, t) holds keys g, g + 8, channels t D/4 .. + D/4 - 1;
+// Which channel or key a lane's fragment element stands for is free as long as
+// both operands agree, so each lane takes contiguous pieces of a row:
+//   K: lane (g, t) holds keys g, g + 8, channels 16 t .. + 15 of each 64;
 //   V: lane (g, t) holds keys 2t, 2t+1, 2t+8, 2t+9, channels g D/8 .. + D/8 - 1.
 // P^T's fragment is S^T's transposed 8 x 8 blocks (movmatrix).
+// A warp copies its tiles (cp.async, 512 bytes in a row per instruction) into a
+// queue of its own in shared memory, one tile ahead, the 16-byte pieces of a row
+// in an order that keeps the fragment reads free of bank conflicts.  (Copies of
+// each lane's own pieces, 8 rows x 64 bytes per instruction, stayed at 4.9 TB/s
+// even without the products; a plain read reaches 6.8.)
 //
 // Codes are exact in f16 (INT8 and E4M3 both).  q is scaled by a power of two
 // per head so that its largest channel lies in [1, 2) and rounded to f16:
@@ -25,9 +29,10 @@
 // (2^-11 relative) is never an underflow of weights that matter.  Sums, row
 // maxima and the output stay in 32 bits.
 //
-// A CTA takes one chunk of keys of one (sequence, KV head); its warps take
-// 16-key tiles in turn and are joined through shared memory; chunks are joined
-// by token_join_kernel in a fixed order (no atomics).
+// A CTA takes one chunk of keys of one segment (a sequence and a KV head with up
+// to 8 * NT of its query heads); its warps take 32-key tiles in turn and are
+// joined through shared memory; chunks are joined by token_join_kernel in a
+// fixed order (no atomics).
 #pragma once
 #include "serve_rows.cuh"
 
@@ -35,8 +40,9 @@ namespace sage {
 
 constexpr int kTokWarps = 4;
 constexpr int kTokThreads = kTokWarps * 32;
-constexpr int kTokTile = 16;              // keys per tile
-constexpr int kTokMaxChunk = 1024;        // keys per CTA
+constexpr int kTokTile = 32;              // keys per tile: two products of 16
+constexpr int kTokStages = 2;             // tiles in a warp's queue
+constexpr int kTokPerSm = 3;              // resident CTAs: the queues take 68 KB each at D = 128
 constexpr float kTokRaise = 8.f;          // the row max moves only when a score passes it by this (log2)
 constexpr float kTokMaxW = 2048.f;        // largest P before its power of two is renewed
 
@@ -55,8 +61,10 @@ struct TokenParams {
   int64_t q_stride, out_stride, table_stride;
   int B, Hq, Hk, G, pages, page_shift;
   int max_len;             // keys that the table can name
-  int chunk, chunks;       // keys per CTA (a multiple of 64), CTAs per (sequence, KV head)
+  int per;                 // tiles of a chunk
+  int chunks;              // chunks that the longest sequence can have
   int head_blocks;         // blocks of 8 * NT query heads per KV head
+  int segs;                // Hk * head_blocks: segments of a sequence
   float scale_log2;        // sm_scale * log2 e
   int* err;
 };
@@ -97,53 +105,79 @@ __device__ __forceinline__ void codes_f16(uint32_t c, uint32_t& lo, uint32_t& hi
   }
 }
 
-// One warp's 16 keys in registers.
-template <int D>
-struct TokTile {
-  uint32_t k[2][D / 16];     // keys g, g + 8: D/4 bytes
-  uint32_t v[4][D / 32];     // keys 2t, 2t+1, 2t+8, 2t+9: D/8 bytes
-  float ks[2], vs[2];        // scales of keys g, g + 8
-  int n;                     // valid keys of the tile (0: none, nothing was read)
-};
-
-template <int kWords>
-__device__ __forceinline__ void ld_words(uint32_t (&w)[kWords], const uint8_t* p) {
-  if constexpr (kWords == 2) {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  } else {
-#pragma unroll
-    for (int i = 0; i < kWords; i += 4)
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "l"(p + 4 * i));
-  }
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
+// A warp's queue.  A stage holds a tile: for each of its two 16-key halves the K
+// rows and the V rows, then the K and the V scale of each key.
 template <int D>
-__device__ __forceinline__ void tok_load(TokTile<D>& x, const TokenParams& p, const int* pages, int first, int n,
-                                         int key, int hk, int g, int t) {
-  x.n = 0;
-  if (key < n) {
-    // Tiles start at multiples of 16 and pages hold a multiple of 16 slots.
-    const int page = pages[((first + key) >> p.page_shift) - (first >> p.page_shift)];
-    if (page >= 0) {
-      x.n = min(kTokTile, n - key);
-      const int off = (first + key) & ((1 << p.page_shift) - 1);
-      const int64_t row = ((static_cast<int64_t>(page) * p.Hk + hk) << p.page_shift) + off;
-      const uint8_t* kp = p.k_codes + (row + g) * D + t * (D / 4);
-      const uint8_t* vp = p.v_codes + (row + 2 * t) * D + g * (D / 8);
-      ld_words(x.k[0], kp);
-      ld_words(x.k[1], kp + 8 * D);
-      x.ks[0] = p.k_scale[row + g];
-      x.ks[1] = p.k_scale[row + g + 8];
-      ld_words(x.v[0], vp);
-      ld_words(x.v[1], vp + D);
-      ld_words(x.v[2], vp + 8 * D);
-      ld_words(x.v[3], vp + 9 * D);
-      x.vs[0] = p.v_scale[row + g];
-      x.vs[1] = p.v_scale[row + g + 8];
+struct TokQueue {
+  static constexpr int kRow = D / 16;                    // 16-byte pieces of a row
+  static constexpr int kV = 16 * D, kHalf = 2 * kV;
+  static constexpr int kScales = 2 * kHalf, kStage = kScales + 2 * 32 * 4;
+  static constexpr int kWarp = kTokStages * kStage, kAll = kTokWarps * kWarp;
+  // Place of piece c of row r: the pieces that eight lanes read at once lie in
+  // different banks.
+  static __device__ __forceinline__ int k_at(int r, int c) { return r * D + (D == 128 ? c ^ ((r & 1) << 2) : c) * 16; }
+  static __device__ __forceinline__ int v_at(int r, int c) {
+    return r * D + (D == 128 ? c ^ (r & 6) : c ^ ((r >> 1) & 3)) * 16;
+  }
+};
+
+// Page table entries of the two halves of a tile at `key` of its sequence, as
+// read; kTokNoKey behind the last key.  They are looked at only when the tile's
+// copies start, a tile later, so that the read is not waited for.
+constexpr int kTokNoKey = -0x7FFFFFFF - 1;
+struct TokPages {
+  int page[2];
+};
+__device__ __forceinline__ TokPages tok_pages(const TokenParams& p, const int32_t* table, int key, int len) {
+  TokPages r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)      // 16-key halves start at multiples of 16, pages hold a multiple of 16 slots
+    r.page[h] = key + 16 * h < len ? table[(key + 16 * h) >> p.page_shift] : kTokNoKey;
+  return r;
+}
+
+// Starts the copies of the tile at `key` into a stage (one group per tile, empty
+// where there is nothing to copy); returns which halves have a page.
+template <int D>
+__device__ __forceinline__ int tok_issue(uint32_t stage, const TokenParams& p, const TokPages& pages, int key, int hk,
+                                         int lane) {
+  using Q = TokQueue<D>;
+  int have = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (pages.page[h] >= 0 && pages.page[h] < p.pages) {
+      have |= 1 << h;
+      const int64_t row = ((static_cast<int64_t>(pages.page[h]) * p.Hk + hk) << p.page_shift) +
+                          ((key + 16 * h) & ((1 << p.page_shift) - 1));
+      const uint32_t dst = stage + h * Q::kHalf;
+#pragma unroll
+      for (int i = 0; i < Q::kRow / 2; ++i) {
+        const int r = (32 * i + lane) / Q::kRow, c = lane % Q::kRow;
+        cp_async<16>(dst + Q::k_at(r, c), p.k_codes + (row + r) * D + c * 16);
+        cp_async<16>(dst + Q::kV + Q::v_at(r, c), p.v_codes + (row + r) * D + c * 16);
+      }
+      // lanes 0-15: the K scales of the half, lanes 16-31: its V scales
+      cp_async<4>(stage + Q::kScales + ((lane >> 4) * 32 + h * 16 + (lane & 15)) * 4,
+                  (lane < 16 ? p.k_scale : p.v_scale) + row + (lane & 15));
+    } else if (pages.page[h] != kTokNoKey) {
+      atomicExch(p.err, 1);
     }
   }
+  cp_async_commit();
+  return have;
 }
 
 // Running state of the lane's heads 2t, 2t + 1 of each block of 8.
@@ -156,340 +190,396 @@ struct TokState {
   float o[NT][D / 16][4];
 };
 
+// n: keys of the tile that exist; have: bit h is set where the page of half h
+// does.  What lies in the other places may be anything: none of it takes part.
 template <int D, int NT, int kFmt>
-__device__ __forceinline__ void tok_step(TokTile<D>& x, const uint32_t (&q)[NT][D / 16][2], const float (&qf)[NT][2],
-                                         TokState<D, NT>& st, int g, int t) {
+__device__ __forceinline__ void tok_step(const uint8_t* stage, int n, int have, const uint32_t (&q)[NT][D / 16][2],
+                                         const float (&qf)[NT][2], TokState<D, NT>& st, int lane) {
+  using Q = TokQueue<D>;
   const float kNegInf = -__int_as_float(0x7F800000);
-  if (x.n < kTokTile) {
-    // Codes and scales behind the last key may be anything: none takes part.
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (2 * t + (i & 1) + 8 * (i >> 1) >= x.n) {
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) x.v[i][k] = 0;
-      }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (g + 8 * i >= x.n) x.vs[i] = 0.f;
-  }
+  const int g = lane >> 2, t = lane & 3;
+  const bool all = n >= kTokTile && have == 3;          // the same in every lane
   uint32_t a[4];
-  float s[NT][4];
+  float s[NT][2][4];
 #pragma unroll
   for (int b = 0; b < NT; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[b][i] = 0.f;
+    for (int i = 0; i < 8; ++i) s[b][i >> 2][i & 3] = 0.f;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    codes_f16<kFmt>(x.k[0][i], a[0], a[2]);
-    codes_f16<kFmt>(x.k[1][i], a[1], a[3]);
+  for (int j = 0; j < D / 64; ++j) {
+    uint32_t k[2][2][4];
 #pragma unroll
-    for (int b = 0; b < NT; ++b) mma_f16_16816(s[b], a, q[b][i][0], q[b][i][1]);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + h * Q::kHalf + Q::k_at(g + 8 * r, 4 * j + t));
+        k[h][r][0] = x.x;
+        k[h][r][1] = x.y;
+        k[h][r][2] = x.z;
+        k[h][r][3] = x.w;
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        codes_f16<kFmt>(k[h][0][i], a[0], a[2]);
+        codes_f16<kFmt>(k[h][1][i], a[1], a[3]);
+#pragma unroll
+        for (int b = 0; b < NT; ++b) mma_f16_16816(s[b][h], a, q[b][4 * j + i][0], q[b][4 * j + i][1]);
+      }
   }
-  uint32_t pb[NT][2];
+  // Keys 16 h + g and 16 h + g + 8: their scales, and whether they are there.
+  float ks[2][2], vs[2][2];
+  bool in[2][2];
+  const float* sc = reinterpret_cast<const float*>(stage + Q::kScales) + g;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      ks[h][r] = sc[16 * h + 8 * r];
+      vs[h][r] = sc[32 + 16 * h + 8 * r];
+      in[h][r] = all || (16 * h + 8 * r + g < n && ((have >> h) & 1));
+      if (!in[h][r]) vs[h][r] = 0.f;
+    }
+  uint32_t pb[NT][2][2];
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
-    // s: (key g, head 2t), (key g, head 2t+1), (key g+8, ..), (key g+8, ..)
-    float e[4];
+    // s[b][h]: (key g, heads 2t, 2t+1), (key g + 8, the same heads)
+    float e[2][4], w[2][4];
     bool raise = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[b][i] = g + 8 * (i >> 1) < x.n ? s[b][i] * x.ks[i >> 1] * qf[b][i & 1] : kNegInf;
-      raise = raise || s[b][i] > st.m[b][i & 1] + kTokRaise;
-    }
-    float w[4];
-    auto weights = [&]() {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float m = st.m[b][i & 1];
-        e[i] = ex2_approx(s[b][i] - (m == kNegInf ? 0.f : m));
-        w[i] = g + 8 * (i >> 1) < x.n ? e[i] * x.vs[i >> 1] * st.cf[b][i & 1] : 0.f;
+        s[b][h][i] = in[h][i >> 1] ? s[b][h][i] * ks[h][i >> 1] * qf[b][i & 1] : kNegInf;
+        raise = raise || s[b][h][i] > st.m[b][i & 1] + kTokRaise;
       }
+    auto weights = [&]() {
+      float big = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float m = st.m[b][i & 1];
+          e[h][i] = ex2_approx(s[b][h][i] - (m == kNegInf ? 0.f : m));
+          w[h][i] = in[h][i >> 1] ? e[h][i] * vs[h][i >> 1] * st.cf[b][i & 1] : 0.f;
+          big = fmaxf(big, w[h][i]);
+        }
+      return big;
     };
     raise = __any_sync(0xFFFFFFFFu, raise);
-    if (!raise) {
-      weights();
-      raise = __any_sync(0xFFFFFFFFu, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])) > kTokMaxW);
-    }
+    if (!raise) raise = __any_sync(0xFFFFFFFFu, weights() > kTokMaxW);
     if (raise) {
       // Renew the reference, and the power of two on the weights, of each head.
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float mx = fmaxf(s[b][h], s[b][h + 2]);
+      for (int c = 0; c < 2; ++c) {
+        float mx = fmaxf(fmaxf(s[b][0][c], s[b][0][c + 2]), fmaxf(s[b][1][c], s[b][1][c + 2]));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-        const float m0 = st.m[b][h], m1 = fmaxf(m0, mx);
+        const float m0 = st.m[b][c], m1 = fmaxf(m0, mx);
         const float ref = m1 == kNegInf ? 0.f : m1;
         const float alpha = m0 == kNegInf ? 0.f : ex2_approx(m0 - ref);
         float wm = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) wm = fmaxf(wm, ex2_approx(s[b][h + 2 * i] - ref) * x.vs[i]);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) wm = fmaxf(wm, ex2_approx(s[b][h][c + 2 * r] - ref) * vs[h][r]);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) wm = fmaxf(wm, __shfl_xor_sync(0xFFFFFFFFu, wm, o));
-        wm = fmaxf(wm, st.w[b][h] * alpha);
+        wm = fmaxf(wm, st.w[b][c] * alpha);
         // exponent of wm in [-100, 100]; wm = 0 keeps the factor
         const int ex = min(max(static_cast<int>(__float_as_uint(wm) >> 23) - 127, -100), 100);
-        const float cf = wm > 0.f ? __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : st.cf[b][h];
+        const float cf = wm > 0.f ? __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : st.cf[b][c];
         // cf is a power of two, so dividing by it is exact
-        const float f = alpha * (cf * (1.f / st.cf[b][h]));
-        st.m[b][h] = m1;
-        st.w[b][h] = wm;
-        st.cf[b][h] = cf;
-        st.l[b][h] *= alpha;
+        const float f = alpha * (cf * (1.f / st.cf[b][c]));
+        st.m[b][c] = m1;
+        st.w[b][c] = wm;
+        st.cf[b][c] = cf;
+        st.l[b][c] *= alpha;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          st.o[b][i][h] *= f;
-          st.o[b][i][h + 2] *= f;
+          st.o[b][i][c] *= f;
+          st.o[b][i][c + 2] *= f;
         }
       }
       weights();
     }
-    st.l[b][0] += e[0] + e[2];
-    st.l[b][1] += e[1] + e[3];
-    pb[b][0] = movmatrix_trans(f16x2_pack(w[0], w[1]));
-    pb[b][1] = movmatrix_trans(f16x2_pack(w[2], w[3]));
-  }
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    // word i of the four keys: channels 4i .. 4i+3 of the lane's D/8
-    const uint32_t lo01 = __byte_perm(x.v[0][i], x.v[1][i], 0x5140), hi01 = __byte_perm(x.v[0][i], x.v[1][i], 0x7362);
-    const uint32_t lo23 = __byte_perm(x.v[2][i], x.v[3][i], 0x5140), hi23 = __byte_perm(x.v[2][i], x.v[3][i], 0x7362);
+    st.l[b][0] += (e[0][0] + e[0][2]) + (e[1][0] + e[1][2]);
+    st.l[b][1] += (e[0][1] + e[0][3]) + (e[1][1] + e[1][3]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      codes_f16<kFmt>(h ? hi01 : lo01, a[0], a[1]);
-      codes_f16<kFmt>(h ? hi23 : lo23, a[2], a[3]);
+      pb[b][h][0] = movmatrix_trans(f16x2_pack(w[h][0], w[h][1]));
+      pb[b][h][1] = movmatrix_trans(f16x2_pack(w[h][2], w[h][3]));
+    }
+  }
 #pragma unroll
-      for (int b = 0; b < NT; ++b) mma_f16_16816(st.o[b][2 * i + h], a, pb[b][0], pb[b][1]);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[4][D / 32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+      const uint8_t* src = stage + h * Q::kHalf + Q::kV +
+                           (D == 128 ? Q::v_at(r, g) : Q::v_at(r, g >> 1) + (g & 1) * 8);
+      if constexpr (D == 128) {
+        const uint4 x = *reinterpret_cast<const uint4*>(src);
+        v[i][0] = x.x;
+        v[i][1] = x.y;
+        v[i][2] = x.z;
+        v[i][3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(src);
+        v[i][0] = x.x;
+        v[i][1] = x.y;
+      }
+    }
+    if (!all) {
+      // Keys 16 h + 2t, 2t + 1, 2t + 8, 2t + 9: a code that is not there may be a NaN.
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (16 * h + 2 * t + (i & 1) + 8 * (i >> 1) >= n || !((have >> h) & 1)) {
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) v[i][k] = 0;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      // word i of the four keys: channels 4i .. 4i+3 of the lane's D/8
+      const uint32_t lo01 = __byte_perm(v[0][i], v[1][i], 0x5140), hi01 = __byte_perm(v[0][i], v[1][i], 0x7362);
+      const uint32_t lo23 = __byte_perm(v[2][i], v[3][i], 0x5140), hi23 = __byte_perm(v[2][i], v[3][i], 0x7362);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        codes_f16<kFmt>(c ? hi01 : lo01, a[0], a[1]);
+        codes_f16<kFmt>(c ? hi23 : lo23, a[2], a[3]);
+#pragma unroll
+        for (int b = 0; b < NT; ++b) mma_f16_16816(st.o[b][2 * i + c], a, pb[b][h][0], pb[b][h][1]);
+      }
     }
   }
 }
 
-// E: type of q and out.  NT: blocks of 8 query heads per CTA.
+template <int D, int NT>
+constexpr int kTokSmem = TokQueue<D>::kAll > kTokWarps * 8 * NT * (D + 4) * 4 ? TokQueue<D>::kAll
+                                                                             : kTokWarps * 8 * NT * (D + 4) * 4;
+
+// Tiles of a sequence.
+__device__ __forceinline__ int tok_tiles(const TokenParams& p, int b) {
+  const int len = min(max(p.lens[b], 0), p.max_len);
+  return (len + kTokTile - 1) / kTokTile;
+}
+
+// E: type of q and out.  NT: blocks of 8 query heads per warp.
 template <class E, int D, int NT, int kFmt>
-__global__ void __launch_bounds__(kTokThreads) token_attn_kernel(const __grid_constant__ TokenParams p) {
+__global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(const __grid_constant__ TokenParams p) {
   pdl_enter();
   using S = typename E::S;
-  __shared__ int s_pages[kTokMaxChunk / kTokTile];
+  using Q = TokQueue<D>;
   __shared__ float s_m[kTokWarps][8 * NT], s_l[kTokWarps][8 * NT];
-  __shared__ float s_o[kTokWarps][8 * NT][D + 4];
+  // The warps' queues; after the last tile the same bytes join the warps' O.
+  extern __shared__ __align__(16) uint8_t tok_smem[];
+  float(*s_o)[8 * NT][D + 4] = reinterpret_cast<float(*)[8 * NT][D + 4]>(tok_smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int b = blockIdx.z;
-  const int hk = blockIdx.y / p.head_blocks;
-  const int h0 = (blockIdx.y - hk * p.head_blocks) * 8 * NT;      // first head of the group
-  const int nh = min(8 * NT, p.G - h0);
-  int len = p.lens[b];
-  if (len > p.max_len) {
-    if (tid == 0) atomicExch(p.err, 1);
-    len = p.max_len;
-  }
-  const int first = blockIdx.x * p.chunk;
-  const int n = min(p.chunk, len - first);
-  if (n <= 0 && (p.chunks > 1 || blockIdx.x > 0)) return;
-
-  const int npg = n > 0 ? ((first + n - 1) >> p.page_shift) - (first >> p.page_shift) + 1 : 0;
-  for (int i = tid; i < npg; i += kTokThreads) {
-    int page = p.table[b * p.table_stride + (first >> p.page_shift) + i];
-    if (page < 0 || page >= p.pages) {
-      atomicExch(p.err, 1);
-      page = -1;
-    }
-    s_pages[i] = page;
-  }
-
-  // Q fragments (heads g of each block of 8) and the factor of the scores.
-  uint32_t q[NT][D / 16][2];
-  float qf[NT][2];
-#pragma unroll
-  for (int blk = 0; blk < NT; ++blk) {
-    const int h = blk * 8 + g;
-    Piece<E, 8> raw[D / 32];
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) raw[i].w[k] = 0;
-      if (h < nh)
-        raw[i].load(static_cast<const S*>(p.q) + b * p.q_stride +
-                    static_cast<int64_t>(hk * p.G + h0 + h) * D + t * (D / 4) + 8 * i);
-      bits = max(bits, piece_amax_bits(raw[i]));
-    }
-    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 1));
-    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 2));
-    // 2^-e, e the exponent of the largest channel (no scaling of zeros and non-finite rows)
-    int ex = static_cast<int>(bits >> 23) - 127;
-    if (ex == 128 || bits == 0) ex = 0;
-    ex = max(ex, -126);
-    const float dn = __uint_as_float(static_cast<uint32_t>(127 - min(ex, 126)) << 23);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-    const float rest = ex == 127 ? 0.5f : 1.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      float f[8];
-      raw[i].get(f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= dn * rest;
-      q[blk][2 * i][0] = f16x2_pack(f[0], f[1]);
-      q[blk][2 * i][1] = f16x2_pack(f[2], f[3]);
-      q[blk][2 * i + 1][0] = f16x2_pack(f[4], f[5]);
-      q[blk][2 * i + 1][1] = f16x2_pack(f[6], f[7]);
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) qf[blk][k] = __shfl_sync(0xFFFFFFFFu, up, (2 * t + k) * 4) * p.scale_log2;
-  }
-  __syncthreads();
-
   const float kNegInf = -__int_as_float(0x7F800000);
-  TokState<D, NT> st;
-#pragma unroll
-  for (int blk = 0; blk < NT; ++blk) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      st.m[blk][k] = kNegInf;
-      st.l[blk][k] = 0.f;
-      st.w[blk][k] = 0.f;
-      st.cf[blk][k] = 1.f;
-    }
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) st.o[blk][i][k] = 0.f;
-  }
-  {
-    TokTile<D> x0, x1;
-    constexpr int kStep = kTokWarps * kTokTile;
-    int key = warp * kTokTile;
-    tok_load<D>(x0, p, s_pages, first, n, key, hk, g, t);
-    while (key < n) {
-      tok_load<D>(x1, p, s_pages, first, n, key + kStep, hk, g, t);
-      if (x0.n > 0) tok_step<D, NT, kFmt>(x0, q, qf, st, g, t);
-      key += kStep;
-      if (key >= n) break;
-      tok_load<D>(x0, p, s_pages, first, n, key + kStep, hk, g, t);
-      if (x1.n > 0) tok_step<D, NT, kFmt>(x1, q, qf, st, g, t);
-      key += kStep;
-    }
-  }
+  const uint8_t* queue = tok_smem + warp * Q::kWarp;
+  const uint32_t qaddr = smem_u32(queue);
 
-  // Join the warps.
+  const int b = blockIdx.z, seg = blockIdx.y;
+  const int tiles = tok_tiles(p, b), tile0 = blockIdx.x * p.per, tile1 = min(tiles, tile0 + p.per);
+  if (tid == 0 && blockIdx.x == 0 && seg == 0 && p.lens[b] > p.max_len) atomicExch(p.err, 1);
+  if (tile0 >= tiles && (p.chunks > 1 || blockIdx.x > 0)) return;
+  {
+    const int len = min(p.lens[b], p.max_len);
+    const int hk = seg / p.head_blocks;
+    const int h0 = (seg - hk * p.head_blocks) * 8 * NT;             // first head of the KV head's
+    const int nh = min(8 * NT, p.G - h0);
+    const int32_t* table = p.table + b * p.table_stride;
+
+    // Pages of the warp's first two tiles, copies of the first.
+    int tile = tile0 + warp;
+    TokPages pg = tok_pages(p, table, tile * kTokTile, tile < tile1 ? len : 0);
+    TokPages next = tok_pages(p, table, (tile + kTokWarps) * kTokTile, tile + kTokWarps < tile1 ? len : 0);
+    int have = tok_issue<D>(qaddr, p, pg, tile * kTokTile, hk, lane);
+
+    // Q fragments (heads g of each block of 8) and the factor of the scores.
+    uint32_t q[NT][D / 16][2];
+    float qf[NT][2];
 #pragma unroll
-  for (int blk = 0; blk < NT; ++blk) {
+    for (int blk = 0; blk < NT; ++blk) {
+      const int h = blk * 8 + g;
+      Piece<E, 8> raw[D / 32];
+      uint32_t bits = 0;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int h = blk * 8 + 2 * t + k;
-      float l = st.l[blk][k];
+      for (int i = 0; i < D / 32; ++i) {
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-      if (g == 0) {
-        s_m[warp][h] = st.m[blk][k];
-        s_l[warp][h] = l;
+        for (int k = 0; k < 4; ++k) raw[i].w[k] = 0;
+        if (h < nh)
+          raw[i].load(static_cast<const S*>(p.q) + b * p.q_stride +
+                      static_cast<int64_t>(hk * p.G + h0 + h) * D + 64 * (i >> 1) + 16 * t + 8 * (i & 1));
+        bits = max(bits, piece_amax_bits(raw[i]));
       }
-      const float up = 1.f / st.cf[blk][k];           // exact: a power of two
+      bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 1));
+      bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 2));
+      // 2^-ex, ex the exponent of the largest channel (no scaling of zeros and non-finite rows)
+      int ex = static_cast<int>(bits >> 23) - 127;
+      if (ex == 128 || bits == 0) ex = 0;
+      ex = max(ex, -126);
+      const float dn = __uint_as_float(static_cast<uint32_t>(127 - min(ex, 126)) << 23);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+      const float rest = ex == 127 ? 0.5f : 1.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        float f[8];
+        raw[i].get(f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] *= dn * rest;
+        q[blk][2 * i][0] = f16x2_pack(f[0], f[1]);
+        q[blk][2 * i][1] = f16x2_pack(f[2], f[3]);
+        q[blk][2 * i + 1][0] = f16x2_pack(f[4], f[5]);
+        q[blk][2 * i + 1][1] = f16x2_pack(f[6], f[7]);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) qf[blk][k] = __shfl_sync(0xFFFFFFFFu, up, (2 * t + k) * 4) * p.scale_log2;
+    }
+
+    TokState<D, NT> st;
+#pragma unroll
+    for (int blk = 0; blk < NT; ++blk) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        st.m[blk][k] = kNegInf;
+        st.l[blk][k] = 0.f;
+        st.w[blk][k] = 0.f;
+        st.cf[blk][k] = 1.f;
+      }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
-        *reinterpret_cast<float2*>(&s_o[warp][h][g * (D / 8) + 2 * i]) =
-            make_float2(st.o[blk][i][k] * up, st.o[blk][i][k + 2] * up);
-    }
-  }
-  __syncthreads();
-  constexpr int kPer = D / 4;                          // lanes of 4 channels per head
-  for (int i = tid; i < nh * kPer; i += kTokThreads) {
-    const int h = i / kPer, d = (i % kPer) * 4;
-    float m = s_m[0][h];
 #pragma unroll
-    for (int w = 1; w < kTokWarps; ++w) m = fmaxf(m, s_m[w][h]);
-    const float ref = m == kNegInf ? 0.f : m;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kTokWarps; ++w) {
-      const float f = ex2_approx(s_m[w][h] - ref);
-      const float4 v = *reinterpret_cast<const float4*>(&s_o[w][h][d]);
-      l += f * s_l[w][h];
-      o.x += f * v.x;
-      o.y += f * v.y;
-      o.z += f * v.z;
-      o.w += f * v.w;
+        for (int k = 0; k < 4; ++k) st.o[blk][i][k] = 0.f;
     }
-    const float r = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
-    const int64_t row = static_cast<int64_t>(b) * p.Hq + hk * p.G + h0 + h;
-    const float lse2 = l == 0.f ? kNegInf : m + log2f(l);
-    o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
-    if (p.chunks > 1) {
-      *reinterpret_cast<float4*>(p.part_o + (row * p.chunks + blockIdx.x) * D + d) = o;
-      if (d == 0) p.part_lse[row * p.chunks + blockIdx.x] = lse2;
-    } else {
-      S* dst = static_cast<S*>(p.out) + b * p.out_stride + static_cast<int64_t>(hk * p.G + h0 + h) * D + d;
-      Piece<E, 4> v;
-      const float f[4] = {o.x, o.y, o.z, o.w};
-      v.put(f);
-      v.store(dst);
-      if (d == 0 && p.lse) p.lse[row] = lse2 * 0.69314718055994531f;
+    static_assert(kTokStages == 2, "the loop keeps one tile ahead");
+    for (int stage = 0; tile < tile1; tile += kTokWarps, stage ^= 1) {
+      const int then = tok_issue<D>(qaddr + (stage ^ 1) * Q::kStage, p, next, (tile + kTokWarps) * kTokTile, hk, lane);
+      next = tok_pages(p, table, (tile + 2 * kTokWarps) * kTokTile, tile + 2 * kTokWarps < tile1 ? len : 0);
+      cp_async_wait<1>();
+      __syncwarp();        // the other lanes' copies too
+      if (have)
+        tok_step<D, NT, kFmt>(queue + stage * Q::kStage, len - tile * kTokTile, have, q, qf, st, lane);
+      have = then;
+      __syncwarp();        // the stage is free
+    }
+    __syncthreads();       // every warp has left its queue
+
+    // Join the warps.
+#pragma unroll
+    for (int blk = 0; blk < NT; ++blk) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int h = blk * 8 + 2 * t + k;
+        float l = st.l[blk][k];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (g == 0) {
+          s_m[warp][h] = st.m[blk][k];
+          s_l[warp][h] = l;
+        }
+        const float up = 1.f / st.cf[blk][k];           // exact: a power of two
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          *reinterpret_cast<float2*>(&s_o[warp][h][g * (D / 8) + 2 * i]) =
+              make_float2(st.o[blk][i][k] * up, st.o[blk][i][k + 2] * up);
+      }
+    }
+    __syncthreads();
+    constexpr int kPer = D / 4;                          // lanes of 4 channels per head
+    for (int i = tid; i < nh * kPer; i += kTokThreads) {
+      const int h = i / kPer, d = (i % kPer) * 4;
+      float m = s_m[0][h];
+#pragma unroll
+      for (int w = 1; w < kTokWarps; ++w) m = fmaxf(m, s_m[w][h]);
+      const float ref = m == kNegInf ? 0.f : m;
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kTokWarps; ++w) {
+        const float f = ex2_approx(s_m[w][h] - ref);
+        const float4 v = *reinterpret_cast<const float4*>(&s_o[w][h][d]);
+        l += f * s_l[w][h];
+        o.x += f * v.x;
+        o.y += f * v.y;
+        o.z += f * v.z;
+        o.w += f * v.w;
+      }
+      const float r = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+      const float lse2 = l == 0.f ? kNegInf : m + log2f(l);
+      o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+      const int head = hk * p.G + h0 + h;
+      const int64_t at = static_cast<int64_t>(b) * p.Hq + head;
+      if (p.chunks == 1) {
+        Piece<E, 4> v;
+        const float f[4] = {o.x, o.y, o.z, o.w};
+        v.put(f);
+        v.store(static_cast<S*>(p.out) + b * p.out_stride + static_cast<int64_t>(head) * D + d);
+        if (d == 0 && p.lse) p.lse[at] = lse2 * 0.69314718055994531f;
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + (at * p.chunks + blockIdx.x) * D + d) = o;
+        if (d == 0) p.part_lse[at * p.chunks + blockIdx.x] = lse2;
+      }
     }
   }
 }
 
-// Joins the chunks of one (sequence, query head): weights 2^(lse_c - max), in
-// chunk order within each of the block's kWays interleaved lanes, then the
-// lanes in order.
+// Joins the chunks of one (sequence, query head), and writes the rows of empty
+// sequences: kWarps warps per row, weights 2^(lse - max), each warp its chunks in
+// order, then the warps in order.
 constexpr int kJoinThreads = 128;
-template <class E, int D>
+template <class E, int D, int kWarps>
 __global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const __grid_constant__ TokenParams p) {
   pdl_enter();
-  constexpr int kLanes = D / 4, kWays = kJoinThreads / kLanes;
-  __shared__ float4 s_o[kWays][kLanes];
-  __shared__ float s_l[kWays];
-  __shared__ float s_red[kJoinThreads / 32];
-  const int64_t row = blockIdx.x;
-  const int b = static_cast<int>(row / p.Hq), h = static_cast<int>(row - static_cast<int64_t>(b) * p.Hq);
-  const int len = min(p.lens[b], p.max_len);
-  const int nc = len > 0 ? (len + p.chunk - 1) / p.chunk : 0;
+  constexpr int V = D / 32;
+  __shared__ float s_o[kWarps][D];
+  __shared__ float s_l[kWarps];
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kJoinThreads / 32 / kWarps) + (threadIdx.x >> 5) / kWarps;
+  if (row >= static_cast<int64_t>(p.B) * p.Hq) return;
+  const int lane = threadIdx.x & 31, way = (threadIdx.x >> 5) % kWarps;
+  const int b = static_cast<int>(row / p.Hq), head = static_cast<int>(row - static_cast<int64_t>(b) * p.Hq);
+  const int parts = (tok_tiles(p, b) + p.per - 1) / p.per;
   const float kNegInf = -__int_as_float(0x7F800000);
   const float* lse = p.part_lse + row * p.chunks;
-  const int tid = threadIdx.x, way = tid / kLanes, d = (tid % kLanes) * 4;
+  const float* part = p.part_o + row * p.chunks * D + lane * V;
   float m = kNegInf;
-  bool nan = false;
-  for (int c = tid; c < nc; c += kJoinThreads) {
-    m = fmaxf(m, lse[c]);
-    nan = nan || lse[c] != lse[c];
-  }
+  for (int i = lane; i < parts; i += 32) m = fmaxf(m, lse[i]);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  if ((tid & 31) == 0) s_red[tid >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, s_red[w]);
   const float ref = m == kNegInf ? 0.f : m;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 4
-  for (int c = way; c < nc; c += kWays) {
-    const float f = ex2_approx(lse[c] - ref);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (row * p.chunks + c) * D + d);
-    l += f;
-    o.x += f * v.x;
-    o.y += f * v.y;
-    o.z += f * v.z;
-    o.w += f * v.w;
-  }
-  s_o[way][tid % kLanes] = o;
-  if (d == 0) s_l[way] = l;
-  __syncthreads();
-  if (way == 0) {
+  float l = 0.f, o[V];
 #pragma unroll
-    for (int w = 1; w < kWays; ++w) {
-      const float4 v = s_o[w][tid];
-      l += s_l[w];
-      o.x += v.x;
-      o.y += v.y;
-      o.z += v.z;
-      o.w += v.w;
-    }
-    const float r = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
-    Piece<E, 4> v;
-    const float f[4] = {o.x * r, o.y * r, o.z * r, o.w * r};
-    v.put(f);
-    v.store(static_cast<typename E::S*>(p.out) + b * p.out_stride + static_cast<int64_t>(h) * D + d);
-    if (d == 0 && p.lse) p.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+  for (int i = 0; i < V; ++i) o[i] = 0.f;
+#pragma unroll 8
+  for (int i = way; i < parts; i += kWarps) {
+    const float f = ex2_approx(lse[i] - ref);
+    l += f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] += f * part[static_cast<int64_t>(i) * D + k];
   }
+  if constexpr (kWarps > 1) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) s_o[way][lane * V + k] = o[k];
+    if (lane == 0) s_l[way] = l;
+    __syncthreads();
+    if (way > 0) return;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      l += s_l[w];
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] += s_o[w][lane * V + k];
+    }
+  }
+  const float r = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] *= r;
+  Piece<E, V> v;
+  v.put(o);
+  v.store(static_cast<typename E::S*>(p.out) + b * p.out_stride + static_cast<int64_t>(head) * D + lane * V);
+  if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace sage
