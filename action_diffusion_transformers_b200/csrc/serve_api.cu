@@ -425,10 +425,10 @@ sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const 
   if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return fail(SAGE_ERR_ALIGNMENT, "lse is not 4-byte aligned");
   int64_t tiles_all = 0;
   for (int i = 0; i < a->n_seq; ++i) tiles_all += (static_cast<int64_t>(cu_q[i + 1]) - cu_q[i] + 255) / 256;
-  if (tiles_all * a->Hq >= (int64_t(1) << 31)) return fail(SAGE_ERR_INVALID_ARG, "too many tiles (Tq * Hq too large)");
-  int dev;
+  if (tiles_all * a->Hq >= (int64_t(1) << 30)) return fail(SAGE_ERR_INVALID_ARG, "too many tiles (Tq * Hq too large)");
+  int dev, sms = 0;
   int* err;
-  if ((st = device_setup(&dev, &err)) != SAGE_OK) return st;
+  if ((st = device_setup(&dev, &err, &sms)) != SAGE_OK) return st;
   if ((st = attn_setup(dev)) != SAGE_OK) return st;
 
   CUtensorMap tq, tk, tv;
@@ -447,6 +447,7 @@ sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const 
   p.lse_stride = Tq;
   p.Hq = a->Hq;
   p.G = a->Hq / a->Hk;
+  p.share = tiles_all * a->Hq > sms ? 1 : 0;
   p.causal = a->causal ? 1 : 0;
   p.scale_log2 = scale_log2(a->sm_scale, a->D);
   p.err = err;
@@ -466,14 +467,32 @@ sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const 
       const int s = order[i];
       const sage::PromptSeq sq = {cu_q[s], cu_k[s], cu_q[s + 1] - cu_q[s], cu_k[s + 1] - cu_k[s]};
       if (sq.lq == 0) continue;
-      tiles += (sq.lq + 2 * sage::kPrTile - 1) / (2 * sage::kPrTile);
+      const int64_t row_tiles = (static_cast<int64_t>(sq.lq) + sage::kPrTile - 1) / sage::kPrTile;
+      tiles += static_cast<int>(((p.share ? row_tiles * p.G : row_tiles) + 1) / 2);
       p.seq[m] = sq;
       p.tile_end[m] = tiles;
       ++m;
     }
     if (tiles == 0) continue;
     p.n_seq = m;
-    const dim3 grid(static_cast<unsigned>(tiles) * a->Hq);
+    p.sorted = tiles <= sage::kPrMaxOrder ? 1 : 0;
+    if (p.sorted) {
+      // Key tiles of a pair's second item, the sort key in front of (sequence, pair).
+      uint64_t keys[sage::kPrMaxOrder];
+      for (int i = 0, t = 0; i < m; ++i) {
+        const sage::PromptSeq& sq = p.seq[i];
+        for (int pair = 0; t < p.tile_end[i]; ++t, ++pair) {
+          const int64_t rt = p.share ? (2 * pair + 1) / p.G : 2 * pair + 1;
+          const int64_t last = std::min<int64_t>((rt + 1) * sage::kPrTile, sq.lq);
+          const int64_t seen = p.causal ? std::max<int64_t>(0, std::min<int64_t>(sq.lk, last + sq.lk - sq.lq)) : sq.lk;
+          keys[t] = static_cast<uint64_t>((seen + sage::kPrTile - 1) / sage::kPrTile) << 32 |
+                    static_cast<uint64_t>(i) << 24 | static_cast<uint64_t>(pair);
+        }
+      }
+      std::sort(keys, keys + tiles, [](uint64_t x, uint64_t y) { return x > y; });
+      for (int t = 0; t < tiles; ++t) p.order[t] = static_cast<uint32_t>(keys[t]);
+    }
+    const dim3 grid(static_cast<unsigned>(tiles) * (p.share ? a->Hk : a->Hq));
     with_flag(a->dtype == SAGE_BF16, [&](auto bf) {
       with_flag(a->D == 128, [&](auto wide) {
         using E = std::conditional_t<bf.value, sage::Bf16T, sage::Fp16T>;
