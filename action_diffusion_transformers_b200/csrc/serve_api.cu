@@ -316,6 +316,7 @@ sage_status sage_rope(sage_rows q, sage_rows k, int T, int D, int dtype, const i
   const int rest = half ? (D - plan->rot_dim + 2 * V - 1) / (2 * V) : D / V - rot_units;
   p.units = rot_units + (in_place ? 0 : rest);
   p.unit_shift = std::min(ceil_log2(p.units), 5);
+  p.pair_stride = (p.pairs + 3) & ~3;
   const int hstep = sage::kRopeThreads >> p.unit_shift;
   // Few tokens: one per CTA, the heads split over grid.y; many: tokens shared by
   // a CTA so that each thread has work behind the angles.
@@ -324,10 +325,9 @@ sage_status sage_rope(sage_rows q, sage_rows k, int T, int D, int dtype, const i
   if (T < 4 * sms) {
     parts = std::min((H + hstep - 1) / hstep, std::max(1, 4 * sms / T));
   } else {
-    p.tokens = std::max(1, std::min({16 * hstep / H, T / (4 * sms), 4096 / p.pairs}));
+    p.tokens = std::max(1, std::min({16 * hstep / H, T / (4 * sms), 4096 / p.pair_stride}));
   }
   p.head_step = (H + parts - 1) / parts;
-  p.pair_stride = (p.pairs + 3) & ~3;
   p.by_pairs = sage::FastDiv(static_cast<uint32_t>(p.pairs));
   p.by_heads = sage::FastDiv(static_cast<uint32_t>(p.head_step));
   parts = (H + p.head_step - 1) / p.head_step;
@@ -422,6 +422,8 @@ sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const 
     SAGE_NEED(k, "k");
     SAGE_NEED(v, "v");
   }
+  if (out == q || (Tk > 0 && (out == k || out == v)))
+    return fail(SAGE_ERR_INVALID_ARG, "out must not be q, k or v");
   if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return fail(SAGE_ERR_ALIGNMENT, "lse is not 4-byte aligned");
   int64_t tiles_all = 0;
   for (int i = 0; i < a->n_seq; ++i) tiles_all += (static_cast<int64_t>(cu_q[i + 1]) - cu_q[i] + 255) / 256;

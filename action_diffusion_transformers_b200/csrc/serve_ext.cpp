@@ -125,6 +125,7 @@ class OnDevice {
     bool first = true;
     for (const int i : tensors) {
       if (args[i] == Py_None) continue;
+      if (!THPVariable_Check(args[i])) refuse(PyExc_TypeError, "a tensor is wanted (got %s)", Py_TYPE(args[i])->tp_name);
       const c10::Device d = THPVariable_Unpack(args[i]).device();
       if (first) {
         if (!d.is_cuda()) refuse(PyExc_ValueError, "tensors must be on a CUDA device (got %s)", d.str().c_str());
@@ -192,7 +193,10 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int dt = 0;
     const at::Tensor* first = nullptr;
     for (int w = 0; w < 2; ++w) {
-      if (a[w] == Py_None) continue;
+      if (a[w] == Py_None) {
+        if (a[4 + w] != Py_None) refuse(PyExc_TypeError, "%s without %s, which must be a tensor", names[w][1], names[w][0]);
+        continue;
+      }
       const at::Tensor &x = tensor(a[w], names[w][0]), &y = tensor(a[4 + w], names[w][1]);
       three_dims(x, names[w][0]);
       if (!first) {

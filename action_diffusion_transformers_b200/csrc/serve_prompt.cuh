@@ -38,8 +38,9 @@
 // Values in masked places: a masked score is replaced, never added to, so K may
 // hold anything there.  A masked weight is 0, but 0 times an infinity or a NaN
 // in a masked V row (a later token, another sequence's row in the same tile)
-// would spread to the row's output; a row whose output is not finite is
-// therefore computed once more from its visible keys alone, in 32 bits.
+// would spread to the row's output; a row whose output is not finite, with a sum
+// that is, is therefore computed once more from its visible keys alone, in 32
+// bits.  (A sum that is not finite comes from the row's own scores.)
 //
 // Every wait is bounded (see mbar_wait_bounded), as in sage_attn.cuh.
 #pragma once
@@ -204,7 +205,7 @@ __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, volatile
 }
 
 // One row once more from its visible keys, 8 channels at a time, in 32 bits:
-// only for rows whose first result was not finite.
+// only for rows whose first result was not finite though their sum was.
 template <class E, int D>
 __device__ __noinline__ void prompt_row_again(const PromptParams& p, const PromptSeq& sq, int row, int h, int visible,
                                               float m, float rl) {
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
           }
         }
-        again = mine && !finite;
+        again = mine && !finite && fabsf(l) < __int_as_float(0x7F800000);
         again_m = m == kNegInf ? 0.f : m;
         again_rl = rl;
         again_row = row;

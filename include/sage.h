@@ -370,7 +370,7 @@ SAGE_API sage_status sage_rope_plan_init(sage_rope_plan* plan, int rot_dim, int 
  *      (left alone in place).  The angle is reduced to a fraction of a
  *      revolution in binary64, so positions far out keep their angle.
  * D a multiple of 8 up to 256, rot_dim <= D.  Rows of `in` and `out` overlap
- * either fully (in place) or not at all.
+ * either fully (in place) or not at all, and those of q and k not at all.
  */
 SAGE_API sage_status sage_rope(sage_rows q, sage_rows k, int T, int D, int dtype, const int64_t* positions,
                                const sage_rope_plan* plan, int transpose, sage_stream_t stream);
@@ -425,8 +425,9 @@ SAGE_API sage_status sage_kv_read(sage_kv_cache cache, const int64_t* slots, int
  *      Tq = cu_q[n_seq], Tk = cu_k[n_seq].
  *      causal: query i of a sequence sees key j when j <= i + Lk - Lq (the ends
  *      are aligned: the queries are the last Lq of Lk tokens); 0: every key.
- *      sm_scale <= 0 selects 1/sqrt(D).
- * out: out [Tq, Hq, D] of the same type; lse f32 [Hq, Tq], the natural log of
+ *      sm_scale <= 0 selects 1/sqrt(D).  The offsets are read during the call: a
+ *      launch captured into a graph keeps them.
+ * out: out [Tq, Hq, D] of the same type, apart from q, k and v; lse f32 [Hq, Tq], the natural log of
  *      the softmax denominator, or NULL.  A query that sees no key gets zeros
  *      and -inf.  Keys it does not see do not reach it, whatever they hold.
  * Scores, sums and output accumulate in 32 bits; the weights are rounded to the

@@ -69,6 +69,21 @@ def test_rope(adt, dtype, T, Hq, Hk, D, r, pairs):
     assert torch.equal(q2, q_out)
 
 
+@pytest.mark.parametrize("D,r,pairs", [(8, 2, True), (8, 2, False), (16, 6, False)])
+def test_rope_of_many_narrow_rows(adt, D, r, pairs):
+    """A million one-head rows: many tokens to a CTA, the angles bounded in shared memory."""
+    T = 1_300_003
+    g = torch.Generator(device="cuda").manual_seed(D)
+    x = torch.randn(T, 1, D, generator=g, device="cuda").half()
+    pos = torch.arange(T, device="cuda")
+    f = 10000.0 ** (-2.0 * torch.arange(r // 2, dtype=torch.float64, device="cuda") / r)
+    got, _ = adt.sage_rope(x, None, pos, adt.RopePlan(r, interleaved=pairs), q_out=torch.empty_like(x))
+    adt.sage_check()
+    ref, size = _rope_ref(x, pos.double()[:, None] * f, 1.0, r, pairs)
+    _rope_check(got, ref, size, r)
+    assert torch.equal(got[..., r:], x[..., r:])
+
+
 @pytest.mark.parametrize("scaling,factor", [(None, 1.0), ("linear", 8.0), ("ntk", 4.0), ("yarn", 16.0)])
 def test_rope_scaling_far_out(adt, scaling, factor):
     T, H, D, r, L0 = 64, 2, 128, 128, 4096

@@ -43,6 +43,11 @@ def _setup(adt, lens, Hq, Hk, D, ps, fmt, dtype, seed=0, garbage=True, spread=0.
     return cache, q, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), slots
 
 
+def _workspace(adt, q, cache, table):
+    n = adt.attn_token_workspace_bytes(q.shape[0], q.shape[1], cache.Hk, cache.D, table.shape[1] * cache.page_size)
+    return torch.empty(max(256, n), dtype=torch.uint8, device="cuda")
+
+
 def _compare(out, lse, cache, q, lens, slots, scale=None):
     B, Hq, D = q.shape
     G = Hq // cache.Hk
@@ -85,8 +90,7 @@ CASES = [
 def test_token(adt, fmt, dtype, lens, Hq, Hk, D, ps):
     cache, q, table, ln, slots = _setup(adt, lens, Hq, Hk, D, ps, fmt, dtype, seed=sum(lens))
     B = len(lens)
-    ws = torch.empty(max(256, adt.attn_token_workspace_bytes(B, Hq, Hk, D, table.shape[1] * ps)), dtype=torch.uint8,
-                     device="cuda")
+    ws = _workspace(adt, q, cache, table)
     out = torch.full((B, Hq, D), 9.0, device="cuda").to(dtype)
     lse = torch.full((B, Hq), 9.0, device="cuda")
     cache.attend(q, table, ln, out, ws, lse=lse)
@@ -116,7 +120,7 @@ def test_v_scales_of_very_different_size(adt, fmt):
     v[:300] *= 3e3
     v[300:310] *= 1e-4
     cache.write(k.bfloat16(), v.bfloat16(), slots)
-    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    ws = _workspace(adt, q, cache, table)
     out, lse = torch.empty_like(q.contiguous()), torch.empty(1, Hq, device="cuda")
     cache.attend(q, table, ln, out, ws, lse=lse, sm_scale=0.5)
     _compare(out, lse, cache, q, [L], slots, scale=0.5)
@@ -129,7 +133,7 @@ def test_queries_of_every_size(adt):
     q = q.clone()
     q[0] *= 1e-30
     q[1] = 0
-    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    ws = _workspace(adt, q, cache, table)
     out, lse = torch.empty_like(q), torch.empty(3, Hq, device="cuda")
     cache.attend(q, table, ln, out, ws, lse=lse)
     _compare(out, lse, cache, q, lens, slots)
@@ -144,7 +148,7 @@ def test_a_poisoned_row_reaches_its_sequence_only(adt):
     bad = torch.full((1, Hk, D), float("inf"), device="cuda", dtype=torch.float16)
     fine = torch.ones_like(bad)
     cache.write(fine, bad, slots[30:31].clone())
-    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    ws = _workspace(adt, q, cache, table)
     out = torch.empty_like(q.contiguous())
     cache.attend(q, table, ln, out, ws)
     assert bool(torch.isnan(out[0]).all()) and bool(torch.isfinite(out[1]).all())
@@ -156,7 +160,7 @@ def test_a_poisoned_row_reaches_its_sequence_only(adt):
 def test_bad_pages_and_lengths_are_left_out_and_reported(adt):
     lens, Hq, Hk, D, ps = [64, 64], 2, 1, 64, 16
     cache, q, table, ln, slots = _setup(adt, lens, Hq, Hk, D, ps, "int8", torch.bfloat16, seed=8)
-    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    ws = _workspace(adt, q, cache, table)
     out = torch.empty_like(q.contiguous())
     lse = torch.empty(2, Hq, device="cuda")
     cache.attend(q, table, ln, out, ws, lse=lse, max_len=64)
@@ -178,7 +182,7 @@ def test_bad_pages_and_lengths_are_left_out_and_reported(adt):
 def test_graph_replay_follows_lens_and_pages(adt):
     lens, Hq, Hk, D, ps = [400, 900], 8, 2, 128, 32
     cache, q, table, ln, slots = _setup(adt, lens, Hq, Hk, D, ps, "int8", torch.bfloat16, seed=12)
-    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    ws = _workspace(adt, q, cache, table)
     out, lse = torch.empty_like(q.contiguous()), torch.empty(2, Hq, device="cuda")
     cache.attend(q, table, ln, out, ws, lse=lse)
     graph = torch.cuda.CUDAGraph()

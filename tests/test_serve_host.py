@@ -149,7 +149,7 @@ def _prompt(adt, cu_q, cu_k=None, **over):
 def test_prompt_refusals(adt):
     L = adt._lib
 
-    def call(p, q=FAKE, k=FAKE, v=FAKE, out=FAKE, lse=None):
+    def call(p, q=FAKE, k=FAKE, v=FAKE, out=2 * FAKE, lse=None):
         return L.sage_attn_prompt(q, k, v, None if p is None else ctypes.byref(p), out, lse, None)
 
     ok = [0, 3, 10]
@@ -170,6 +170,10 @@ def test_prompt_refusals(adt):
     for name in ("q", "k", "v", "out"):
         assert call(_prompt(adt, ok), **{name: None}) == 1 and call(_prompt(adt, ok), **{name: FAKE + 2}) == 3
     assert call(_prompt(adt, ok), lse=FAKE + 2) == 3
+    for name in ("q", "k", "v"):                                   # out on top of an input
+        ptrs = dict(q=FAKE, k=2 * FAKE, v=3 * FAKE, out=4 * FAKE)
+        ptrs["out"] = ptrs[name]
+        assert call(_prompt(adt, ok), **ptrs) == 1 and b"out" in L.sage_last_error()
     assert call(_prompt(adt, [0]), q=None) == 0 and call(_prompt(adt, [0, 0], [0, 7]), q=None) == 0
     if not _gpu():
         assert call(_prompt(adt, ok)) == 4
@@ -252,6 +256,8 @@ def test_python_layer_refuses_layouts(adt):
         rope(q=None, k=None)
     with pytest.raises(ValueError, match="q_out"):
         rope(q_out=narrow)
+    with pytest.raises(TypeError, match="tensor"):
+        rope(q=None, q_out=5)
     with pytest.raises(ValueError, match="positions"):
         rope(pos=slots.int())
     with pytest.raises(ValueError, match="positions"):
