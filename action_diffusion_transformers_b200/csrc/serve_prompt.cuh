@@ -262,7 +262,6 @@ template <class E, int D>
 __global__ void __launch_bounds__(kPrThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PromptParams p) {
-  pdl_enter();
   using L = PrSmem<D>;
   using S = typename E::S;
   constexpr int kSlots = L::kSlots;
@@ -323,10 +322,18 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  if (tid == 32 * kPrWarpLoad) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // Up to here nothing of the caller's was read: the set-up above may run beside
+  // the kernel before.
+  pdl_enter();
 
   bool again = false;                      // this thread's row has to be computed once more
   float again_m = 0.f, again_rl = 0.f;
@@ -336,9 +343,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
    if (warp == kPrWarpLoad) {
     // ------------------------------------------------------------ loads
     if (lane == 0 && n > 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
       auto load = [&](uint8_t* dst, const CUtensorMap* tm, int head, int row, uint64_t* bar) {
         mbar_arrive_expect_tx(bar, L::kTileBytes);
 #pragma unroll

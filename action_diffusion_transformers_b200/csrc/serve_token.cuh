@@ -141,6 +141,11 @@ constexpr int kTokNoKey = -0x7FFFFFFF - 1;
 struct TokPages {
   int page[2];
 };
+__device__ __forceinline__ void tok_cut(TokPages& r, int key, int len) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (key + 16 * h >= len) r.page[h] = kTokNoKey;
+}
 __device__ __forceinline__ TokPages tok_pages(const TokenParams& p, const int32_t* table, int key, int len) {
   TokPages r;
 #pragma unroll
@@ -383,20 +388,35 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
   const uint32_t qaddr = smem_u32(queue);
 
   const int b = blockIdx.z, seg = blockIdx.y;
-  const int tiles = tok_tiles(p, b), tile0 = blockIdx.x * p.per, tile1 = min(tiles, tile0 + p.per);
-  if (tid == 0 && blockIdx.x == 0 && seg == 0 && p.lens[b] > p.max_len) atomicExch(p.err, 1);
-  if (tile0 >= tiles && (p.chunks > 1 || blockIdx.x > 0)) return;
+  const int hk = seg / p.head_blocks;
+  const int h0 = (seg - hk * p.head_blocks) * 8 * NT;             // first head of the KV head's
+  const int nh = min(8 * NT, p.G - h0);
+  const int32_t* table = p.table + b * p.table_stride;
+  const int tile0 = blockIdx.x * p.per;
   {
-    const int len = min(p.lens[b], p.max_len);
-    const int hk = seg / p.head_blocks;
-    const int h0 = (seg - hk * p.head_blocks) * 8 * NT;             // first head of the KV head's
-    const int nh = min(8 * NT, p.G - h0);
-    const int32_t* table = p.table + b * p.table_stride;
-
-    // Pages of the warp's first two tiles, copies of the first.
+    // The length, the pages of the warp's first two tiles and its part of Q are
+    // read side by side; pages behind the length are dropped once it is there.
     int tile = tile0 + warp;
-    TokPages pg = tok_pages(p, table, tile * kTokTile, tile < tile1 ? len : 0);
-    TokPages next = tok_pages(p, table, (tile + kTokWarps) * kTokTile, tile + kTokWarps < tile1 ? len : 0);
+    const int all = p.lens[b];
+    TokPages pg = tok_pages(p, table, tile * kTokTile, warp < p.per ? p.max_len : 0);
+    TokPages next = tok_pages(p, table, (tile + kTokWarps) * kTokTile, warp + kTokWarps < p.per ? p.max_len : 0);
+    Piece<E, 8> raw[NT][D / 32];
+#pragma unroll
+    for (int blk = 0; blk < NT; ++blk)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) raw[blk][i].w[k] = 0;
+        if (blk * 8 + g < nh)
+          raw[blk][i].load(static_cast<const S*>(p.q) + b * p.q_stride +
+                           static_cast<int64_t>(hk * p.G + h0 + blk * 8 + g) * D + 64 * (i >> 1) + 16 * t + 8 * (i & 1));
+      }
+    if (tid == 0 && blockIdx.x == 0 && seg == 0 && all > p.max_len) atomicExch(p.err, 1);
+    const int len = min(max(all, 0), p.max_len);
+    const int tiles = (len + kTokTile - 1) / kTokTile, tile1 = min(tiles, tile0 + p.per);
+    if (tile0 >= tiles && (p.chunks > 1 || blockIdx.x > 0)) return;
+    tok_cut(pg, tile * kTokTile, len);
+    tok_cut(next, (tile + kTokWarps) * kTokTile, len);
     int have = tok_issue<D>(qaddr, p, pg, tile * kTokTile, hk, lane);
 
     // Q fragments (heads g of each block of 8) and the factor of the scores.
@@ -404,18 +424,9 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
     float qf[NT][2];
 #pragma unroll
     for (int blk = 0; blk < NT; ++blk) {
-      const int h = blk * 8 + g;
-      Piece<E, 8> raw[D / 32];
       uint32_t bits = 0;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) raw[i].w[k] = 0;
-        if (h < nh)
-          raw[i].load(static_cast<const S*>(p.q) + b * p.q_stride +
-                      static_cast<int64_t>(hk * p.G + h0 + h) * D + 64 * (i >> 1) + 16 * t + 8 * (i & 1));
-        bits = max(bits, piece_amax_bits(raw[i]));
-      }
+      for (int i = 0; i < D / 32; ++i) bits = max(bits, piece_amax_bits(raw[blk][i]));
       bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 1));
       bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, 2));
       // 2^-ex, ex the exponent of the largest channel (no scaling of zeros and non-finite rows)
@@ -428,7 +439,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         float f[8];
-        raw[i].get(f);
+        raw[blk][i].get(f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] *= dn * rest;
         q[blk][2 * i][0] = f16x2_pack(f[0], f[1]);

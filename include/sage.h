@@ -454,7 +454,7 @@ SAGE_API sage_status sage_attn_prompt(const void* q, const void* k, const void* 
  *      the cache's Hk.  page_table int32 [B, table_stride]: entry i is the page
  *      of tokens i * page_size ..; lens int32 [B]: keys 0 .. lens[b] - 1 are
  *      seen (0 or less: none).  Only the first ceil(lens[b] / page_size) entries
- *      of a row are read.  max_len: an upper bound on lens, at most
+ *      of a row count, the others may hold anything.  max_len: an upper bound on lens, at most
  *      table_stride * page_size (longer lens are cut there and recorded); it
  *      sets the launch and the workspace.  sm_scale <= 0 selects 1/sqrt(D).
  * out: out [B, Hq, D] of q's type; lse f32 [B, Hq] or NULL; zeros and -inf for a
