@@ -202,6 +202,110 @@ sage_status check_scale(float s) {
   return SAGE_OK;
 }
 
+// Row tile of an item (row tile, head) of a sequence.
+int64_t prompt_row_tile(const sage::PromptParams& p, int item) { return p.share ? item / p.G : item; }
+
+// Work of one CTA of the prompt kernel, for sorting: its time in halves of a pair's
+// step over one key tile (an item alone takes half of them, its key tiles going to
+// both tiles of the CTA) plus about one step for its start and end, in front of
+// (sequence, which, pair).
+uint64_t prompt_key(const sage::PromptParams& p, int i, int pair, uint32_t which) {
+  const sage::PromptSeq& sq = p.seq[i];
+  int64_t rt = prompt_row_tile(p, 2 * pair + (which == sage::kPrFirst ? 0 : 1));
+  bool alone = which != sage::kPrBoth;
+  if (!alone && rt * sage::kPrTile >= sq.lq) {
+    rt = prompt_row_tile(p, 2 * pair);                             // a pair without its second item
+    alone = true;
+  }
+  const int64_t last = std::min<int64_t>((rt + 1) * sage::kPrTile, sq.lq);
+  const int64_t seen = p.causal ? std::max<int64_t>(0, std::min<int64_t>(sq.lk, last + sq.lk - sq.lq)) : sq.lk;
+  const int64_t n = (seen + sage::kPrTile - 1) / sage::kPrTile;
+  return static_cast<uint64_t>(alone ? n + 3 : 2 * n + 2) << 32 | static_cast<uint64_t>(i) << 24 | which << 20 |
+         static_cast<uint64_t>(pair);
+}
+
+// End of each entry's last CTA when the CTAs (`lanes` of each entry, in order)
+// start one after the other on the SM that is free first; returns the last end.
+constexpr int kPrBalance = 128, kPrBalanceSms = 256;
+int64_t prompt_ends(const uint64_t* keys, int n, int lanes, int sms, int64_t* ends) {
+  struct Group {
+    int64_t t;
+    int count;
+  } heap[kPrBalanceSms];                                 // SMs by the time at which they are free
+  auto later = [](const Group& x, const Group& y) { return x.t > y.t; };
+  int groups = 1;
+  heap[0] = {0, sms};
+  int64_t all = 0;
+  for (int e = 0; e < n; ++e) {
+    const int64_t cost = static_cast<int64_t>(keys[e] >> 32);
+    Group done[kPrBalanceSms];
+    int nd = 0, need = lanes;
+    ends[e] = 0;
+    while (need > 0) {
+      if (groups == 0) {                                 // more CTAs of an entry than SMs
+        for (; nd > 0; --nd) {
+          heap[groups++] = done[nd - 1];
+          std::push_heap(heap, heap + groups, later);
+        }
+      }
+      std::pop_heap(heap, heap + groups, later);
+      Group g = heap[--groups];
+      const int take = std::min(g.count, need);
+      need -= take;
+      done[nd++] = {g.t + cost, take};
+      ends[e] = std::max(ends[e], g.t + cost);
+      if (g.count > take) {
+        heap[groups++] = {g.t, g.count - take};
+        std::push_heap(heap, heap + groups, later);
+      }
+    }
+    for (; nd > 0; --nd) {
+      heap[groups++] = done[nd - 1];
+      std::push_heap(heap, heap + groups, later);
+    }
+    all = std::max(all, ends[e]);
+  }
+  return all;
+}
+
+// Sorts the entries, the longest first, and parts pairs whose end stands out into
+// their two items, as long as that brings the last end forward.  Returns the
+// number of entries.  Only for launches of few waves, where it counts.
+int prompt_balance(const sage::PromptParams& p, uint64_t* keys, int n, int lanes, int sms) {
+  auto larger = [](uint64_t x, uint64_t y) { return x > y; };
+  std::sort(keys, keys + n, larger);
+  if (n > kPrBalance || sms > kPrBalanceSms || static_cast<int64_t>(n) * lanes > 6 * static_cast<int64_t>(sms)) return n;
+  int64_t ends[2 * kPrBalance];
+  uint64_t next[2 * kPrBalance];
+  int64_t all = prompt_ends(keys, n, lanes, sms, ends);
+  for (int pass = 0; pass < 3; ++pass) {
+    int64_t work = 0;
+    for (int e = 0; e < n; ++e) work += static_cast<int64_t>(keys[e] >> 32) * lanes;
+    const int64_t ideal = std::max(work / sms, static_cast<int64_t>(keys[0] >> 32) / 2), limit = ideal + ideal / 16;
+    if (all <= limit) break;
+    int m = 0;
+    for (int e = 0; e < n; ++e) {
+      const int seq = static_cast<int>(keys[e] >> 24 & 0xFF), pair = static_cast<int>(keys[e] & 0xFFFFF);
+      const bool both = (keys[e] >> 20 & 3) == sage::kPrBoth &&
+                        prompt_row_tile(p, 2 * pair + 1) * sage::kPrTile < p.seq[seq].lq;
+      if (both && ends[e] > limit && m + n - e < 2 * kPrBalance) {
+        next[m++] = prompt_key(p, seq, pair, sage::kPrFirst);
+        next[m++] = prompt_key(p, seq, pair, sage::kPrSecond);
+      } else {
+        next[m++] = keys[e];
+      }
+    }
+    if (m == n) break;
+    std::sort(next, next + m, larger);
+    const int64_t now = prompt_ends(next, m, lanes, sms, ends);
+    if (now >= all) break;
+    all = now;
+    n = m;
+    std::copy(next, next + m, keys);
+  }
+  return n;
+}
+
 }  // namespace
 
 extern "C" {
@@ -454,6 +558,7 @@ sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const 
   p.scale_log2 = scale_log2(a->sm_scale, a->D);
   p.err = err;
   p.timeout_ns = sage_host::wait_timeout_ns();
+  const int lanes = p.share ? a->Hk : a->Hq;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   for (int base = 0; base < a->n_seq; base += sage::kPrMaxSeq) {
     const int n = std::min(sage::kPrMaxSeq, a->n_seq - base);
@@ -479,22 +584,13 @@ sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const 
     p.n_seq = m;
     p.sorted = tiles <= sage::kPrMaxOrder ? 1 : 0;
     if (p.sorted) {
-      // Key tiles of a pair's second item, the sort key in front of (sequence, pair).
       uint64_t keys[sage::kPrMaxOrder];
-      for (int i = 0, t = 0; i < m; ++i) {
-        const sage::PromptSeq& sq = p.seq[i];
-        for (int pair = 0; t < p.tile_end[i]; ++t, ++pair) {
-          const int64_t rt = p.share ? (2 * pair + 1) / p.G : 2 * pair + 1;
-          const int64_t last = std::min<int64_t>((rt + 1) * sage::kPrTile, sq.lq);
-          const int64_t seen = p.causal ? std::max<int64_t>(0, std::min<int64_t>(sq.lk, last + sq.lk - sq.lq)) : sq.lk;
-          keys[t] = static_cast<uint64_t>((seen + sage::kPrTile - 1) / sage::kPrTile) << 32 |
-                    static_cast<uint64_t>(i) << 24 | static_cast<uint64_t>(pair);
-        }
-      }
-      std::sort(keys, keys + tiles, [](uint64_t x, uint64_t y) { return x > y; });
+      for (int i = 0, t = 0; i < m; ++i)
+        for (int pair = 0; t < p.tile_end[i]; ++t, ++pair) keys[t] = prompt_key(p, i, pair, sage::kPrBoth);
+      tiles = prompt_balance(p, keys, tiles, lanes, sms);
       for (int t = 0; t < tiles; ++t) p.order[t] = static_cast<uint32_t>(keys[t]);
     }
-    const dim3 grid(static_cast<unsigned>(tiles) * (p.share ? a->Hk : a->Hq));
+    const dim3 grid(static_cast<unsigned>(tiles * lanes));
     with_flag(a->dtype == SAGE_BF16, [&](auto bf) {
       with_flag(a->D == 128, [&](auto wide) {
         using E = std::conditional_t<bf.value, sage::Bf16T, sage::Fp16T>;

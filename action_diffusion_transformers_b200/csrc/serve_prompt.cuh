@@ -11,7 +11,11 @@
 // heads running fastest, so that both tiles see about the same keys; where that
 // would leave SMs idle (no more CTAs than SMs with a CTA per two row tiles of one
 // head) the row tiles of one head are paired instead: 144 against 96 CTAs for
-// eight captions x 16 heads, 8.8 against 10.0 us.  384 threads:
+// eight captions x 16 heads, 8.8 against 10.0 us.  An item alone (a pair without
+// its second, or one that the host parts because its end would stand out) gives
+// its even key tiles to A, its odd ones to B, and the two are joined at the end:
+// 1024 tokens x 24 heads 25.7 to 19.4 us, chunks of 32 to 1504 tokens behind up to
+// 3000 earlier ones x 24 heads 112.5 to 104.7.  384 threads:
 //   warps 0-3, 4-7  softmax of tile A, of tile B: thread r owns query row r
 //                   (TMEM lane r), reads its 128 scores, writes P back as
 //                   16-bit pairs over the first 64 score columns, 64 keys at a
@@ -74,6 +78,10 @@ struct PrSmem {
 };
 static_assert(PrSmem<128>::kAlloc <= 232448 && PrSmem<64>::kAlloc <= 232448, "shared memory of one CTA");
 
+// What a CTA takes of a pair of items: both, or one alone, whose key tiles then
+// go to the two tiles in turn (see the kernel).
+enum PromptWhich : uint32_t { kPrBoth = 0, kPrFirst = 1, kPrSecond = 2 };
+
 struct PromptSeq {
   int q0, k0, lq, lk;       // first rows and lengths
 };
@@ -94,7 +102,7 @@ struct PromptParams {
   PromptSeq seq[kPrMaxSeq];
   int tile_end[kPrMaxSeq];  // pairs (per KV head, or per head) up to and including a sequence
   int sorted;               // 1: order[] holds the pairs, most key tiles first
-  uint32_t order[kPrMaxOrder];   // sequence << 24 | pair
+  uint32_t order[kPrMaxOrder];   // sequence << 24 | which << 20 | pair (see PromptWhich)
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
@@ -141,8 +149,8 @@ __device__ __forceinline__ uint64_t make_sdesc_mn(uint32_t saddr, uint32_t piece
 // (fitted by linear programming), n added to the exponent field.  Cubic (1.0e-4)
 // where the weights are rounded to bf16 (2^-9), quartic (2.8e-6) for fp16
 // (2^-12).  Two pairs of each 16: on 8192 tokens x 32 heads, D = 128 / 64, none
-// takes 574 / 501 us, two 558 / 480, four 558 / 479, six 557 / 487, eight (an
-// earlier kernel) 691: the FMA pipe, at 3 cycles a packed operation, fills up.
+// takes 549 / 406 us, two 536 / 400, four 559 / 411 (the FMA pipe, at 3 cycles a
+// packed operation, fills up); eight captions take 7.6 / 7.8 / 7.8.
 constexpr int kPrPolyOf16 = 2;
 __host__ __device__ constexpr bool pr_on_fma(int i) { return (i * kPrPolyOf16) % 16 < kPrPolyOf16; }
 template <bool kCubic>
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PromptParams p) {
   using L = PrSmem<D>;
   using S = typename E::S;
-  constexpr int kSlots = L::kSlots;
+  constexpr int kSlots = L::kSlots, kHalf = kSlots / 2;
   constexpr bool kBf16 = std::is_same<E, Bf16T>::value;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -281,9 +289,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   const int tile = blockIdx.x / lanes;
   const int hb = blockIdx.x - tile * lanes;
   int lo = 0, pair;
+  uint32_t which = kPrBoth;
   if (p.sorted) {
     lo = p.order[tile] >> 24;
-    pair = p.order[tile] & 0xFFFFFF;
+    which = (p.order[tile] >> 20) & 3;
+    pair = p.order[tile] & 0xFFFFF;
   } else {
     int hi = p.n_seq - 1;
     while (lo < hi) {
@@ -298,18 +308,31 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   const int hk = p.share ? hb : hb / p.G;
   // First row and head of the two tiles, and the key tiles that the last row of
   // each sees.
+  const int first = 2 * pair + (which == kPrSecond ? 1 : 0);
+  const bool alone =
+      which != kPrBoth || (p.share ? (first + 1) / p.G : first + 1) * static_cast<int64_t>(kPrTile) >= sq.lq;
   int rows[2], heads[2], nt[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int i = 2 * pair + x;
+    const int i = alone ? first : first + x;
     const int rt = p.share ? i / p.G : i;
     heads[x] = p.share ? hb * p.G + (i - rt * p.G) : hb;
     rows[x] = rt * kPrTile;
     const int last = min(rows[x] + kPrTile, sq.lq) - 1;
     const int seen = p.causal ? min(sq.lk, last + off + 1) : sq.lk;
-    nt[x] = rows[x] < sq.lq && seen > 0 ? (seen + kPrTile - 1) / kPrTile : 0;
+    nt[x] = seen > 0 ? (seen + kPrTile - 1) / kPrTile : 0;
   }
   const int n = max(nt[0], nt[1]);
+  // An item alone: tile A takes its even key tiles, tile B the odd ones, each
+  // with half of the ring, and the two are joined at the end.
+  const bool split = alone && n > 1;
+  if (split) {
+    nt[0] = (n + 1) / 2;
+    nt[1] = n / 2;
+  } else if (alone) {
+    nt[1] = 0;
+    rows[1] = sq.lq;                                    // no rows
+  }
 
   if (warp == kPrWarpMma) {
     tmem_alloc(tmem_slot, 512);
@@ -317,8 +340,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < L::kNumBars; ++i)
-      // P, S read: one arrival per softmax warp; a ring slot is empty when both tiles have read it
-      mbar_init(&bars[i], i >= L::kPFull && i < L::kFull ? 4 : i >= L::kEmpty && i < L::kDrain ? 2 : 1);
+      // P, S read: one arrival per softmax warp; a ring slot is empty when all tiles that read it have
+      mbar_init(&bars[i], i >= L::kPFull && i < L::kFull ? 4 : i >= L::kEmpty && i < L::kDrain && !split ? 2 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -348,16 +371,19 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * kPrTile * 128, tm, c * 64, head, row, bar);
       };
-      int issued = 0;
+      uint32_t issued = 0, parity = 0;                  // bit per slot: loaded, parity of its last load
       for (int it = 0; it < 2 * n; ++it) {
-        const int slot = it % kSlots;
-        const uint32_t use = static_cast<uint32_t>(it / kSlots);
+        // Split: loads 0, 1, 4, 5, ... are tile A's, its own loads 0, 1, 2, 3, ...
+        const int own = split ? (it >> 2) * 2 + (it & 1) : it;
+        const int slot = split ? ((it >> 1) & 1) * kHalf + own % kHalf : own % kSlots;
+        const uint32_t use = static_cast<uint32_t>(split ? own / kHalf : own / kSlots);
         if (it == 0 && nt[0] > 0) load(smem + L::kQ, &tm_q, heads[0], sq.q0 + rows[0], &bars[L::kQFull]);
         if (use > 0 && !mbar_wait_bounded(&bars[L::kEmpty + slot], (use - 1) & 1, abort_flag, tmo)) break;
         load(smem + L::kRing + slot * L::kTileBytes, (it & 1) ? &tm_v : &tm_k, hk, sq.k0 + (it >> 1) * kPrTile,
              &bars[L::kFull + slot]);
-        issued = it + 1;
-        if (it == 0 && nt[1] > 0)
+        issued |= 1u << slot;
+        parity = (parity & ~(1u << slot)) | (use & 1) << slot;
+        if (it == 0 && nt[1] > 0 && !split)
           load(smem + L::kQ + L::kTileBytes, &tm_q, heads[1], sq.q0 + rows[1], &bars[L::kQFull + 1]);
       }
       if (*abort_flag) {
@@ -366,11 +392,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         int none = 0;
         volatile int* nf = reinterpret_cast<volatile int*>(&none);
         if (nt[0] > 0) mbar_wait_bounded(&bars[L::kQFull], 0, nf, drain);
-        if (nt[1] > 0) mbar_wait_bounded(&bars[L::kQFull + 1], 0, nf, drain);
-        for (int slot = 0; slot < kSlots && slot < issued; ++slot) {
-          const int last = (issued - 1 - slot) / kSlots;
-          mbar_wait_bounded(&bars[L::kFull + slot], static_cast<uint32_t>(last) & 1, nf, drain);
-        }
+        if (nt[1] > 0 && !split) mbar_wait_bounded(&bars[L::kQFull + 1], 0, nf, drain);
+        for (int slot = 0; slot < kSlots; ++slot)
+          if (issued >> slot & 1) mbar_wait_bounded(&bars[L::kFull + slot], parity >> slot & 1, nf, drain);
       }
     }
    } else if (warp < kPrWarpLoad) {
@@ -378,16 +402,18 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     if (lane == 0 && n > 0) {
       const int x = warp - kPrWarpMma;
       const int ntx = x ? nt[1] : nt[0];
+      const int steps = split ? ntx : n;              // key tiles whose slots this tile gives back
+      const int qx = split ? 0 : x;
       constexpr uint32_t kFmt = kBf16 ? 1u : 0u;
       constexpr uint32_t kIdescQK = make_idesc(1u, kFmt, 128u, 128u);
       constexpr uint32_t kIdescPV = make_idesc(1u, kFmt, 128u, static_cast<uint32_t>(D)) | (1u << 16);
       auto wait = [&](int bar, int phase) {
         return mbar_wait_bounded(&bars[bar], static_cast<uint32_t>(phase) & 1, abort_flag, tmo);
       };
-      auto slot_of = [&](int it) { return it % kSlots; };
-      auto wait_full = [&](int it) { return wait(L::kFull + slot_of(it), it / kSlots); };
+      auto slot_of = [&](int it) { return split ? x * kHalf + it % kHalf : it % kSlots; };
+      auto wait_full = [&](int it) { return wait(L::kFull + slot_of(it), split ? it / kHalf : it / kSlots); };
       auto scores = [&](int j) {                  // S_x(j) = Q_x K_j^T
-        const uint64_t qd = make_sdesc(smem_u32(smem + L::kQ + x * L::kTileBytes), 1024u, 2u);
+        const uint64_t qd = make_sdesc(smem_u32(smem + L::kQ + qx * L::kTileBytes), 1024u, 2u);
         const uint64_t kd = make_sdesc(smem_u32(smem + L::kRing + slot_of(2 * j) * L::kTileBytes), 1024u, 2u);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -405,23 +431,23 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-            mma_f16_ts(tmem + L::kColO + x * L::kStepO, tmem + L::kColP + x * L::kStepP + kk * 8, vd + kk * (16 * 128 / 16), kIdescPV,
-                       (j > 0 || kk > 0) ? 1u : 0u);
+            mma_f16_ts(tmem + L::kColO + x * L::kStepO, tmem + L::kColP + x * L::kStepP + kk * 8,
+                       vd + kk * (16 * 128 / 16), kIdescPV, (j > 0 || kk > 0) ? 1u : 0u);
         }
         tc_commit(&bars[L::kPVDone + x]);
         return true;
       };
       // A commit arrives when all that this thread issued before has completed
       // (at once for a tile without work), so each slot is given back by both.
-      bool ok = wait_full(0) && (ntx == 0 || wait(L::kQFull + x, 0));
+      bool ok = wait_full(0) && (ntx == 0 || wait(L::kQFull + qx, 0));
       if (ok && ntx > 0) {
         tc_fence_after();
         scores(0);
       }
       if (ok) tc_commit(&bars[L::kEmpty + slot_of(0)]);
-      for (int j = 0; ok && j < n; ++j) {
+      for (int j = 0; ok && j < steps; ++j) {
         if constexpr (L::kApart) {
-          if (j + 1 < n) {
+          if (j + 1 < steps) {
             if (!(ok = wait_full(2 * j + 2) && (j + 1 >= ntx || wait(L::kSRead + x, j)))) break;
             if (j + 1 < ntx) {
               tc_fence_after();
@@ -435,7 +461,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           // What is on the way from P_x(j) to S_x(j+1) is kept short: K_j+1 is
           // waited for before, V_j given back after (a wait on a completed barrier
           // takes about 120 cycles, a commit behind products up to 300).
-          if (!(ok = (j + 1 >= n || wait_full(2 * j + 2)) && wait_full(2 * j + 1) && (j >= ntx || products(j)))) break;
+          if (!(ok = (j + 1 >= steps || wait_full(2 * j + 2)) && wait_full(2 * j + 1) && (j >= ntx || products(j)))) break;
           if (j + 1 < ntx) {
             // S_x(j+1) takes the columns that hold P_x(j): wait for its products.
             if (!(ok = wait(L::kPVDone + x, j))) break;
@@ -443,7 +469,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             scores(j + 1);
           }
           tc_commit(&bars[L::kEmpty + slot_of(2 * j + 1)]);
-          if (j + 1 < n) tc_commit(&bars[L::kEmpty + slot_of(2 * j + 2)]);
+          if (j + 1 < steps) tc_commit(&bars[L::kEmpty + slot_of(2 * j + 2)]);
         }
       }
       tc_commit(&bars[L::kDrain + x]);
@@ -483,7 +509,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kSRead + x]);
       }
-      const int valid = visible - j * kPrTile;
+      const int valid = visible - (split ? 2 * j + x : j) * kPrTile;
       const bool masked = __any_sync(0xFFFFFFFFu, valid < kPrTile);
       if (masked) {
 #pragma unroll
@@ -543,17 +569,46 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     S* dst = static_cast<S*>(p.out) + static_cast<int64_t>(sq.q0 + row) * p.out_stride + static_cast<int64_t>(head) * D;
     if (ntx > 0) {
       if (ok) ok = pr_wait(&bars[L::kPVDone + x], static_cast<uint32_t>(ntx - 1) & 1, abort_flag, tmo);
+      int cb0 = 0, cb1 = D;                              // channels that this thread stores
+      float wa = 1.f, wb = 0.f;                          // split: weights of O_A, O_B
+      if (split) {
+        // O = (2^(m_A - m) O_A + 2^(m_B - m) O_B) / l, l alike, m the larger of the
+        // two: thread r of tile A takes the first half of the channels of row r, of
+        // tile B the second; both reach that TMEM lane.  Every softmax warp comes
+        // here, after a wait that ran out too.  Q_B's place is free.
+        float2* stat = reinterpret_cast<float2*>(smem + L::kQ + L::kTileBytes);
+        stat[x * kPrTile + r] = make_float2(m, l);
+        tc_fence_before();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float2 a = stat[r], b = stat[kPrTile + r];
+        m = fmaxf(a.x, b.x);
+        wa = a.x == kNegInf ? 0.f : ex2_approx(a.x - m);
+        wb = b.x == kNegInf ? 0.f : ex2_approx(b.x - m);
+        l = fmaf(a.y, wa, b.y * wb);
+        cb0 = x * (D / 2);
+        cb1 = cb0 + D / 2;
+      }
       if (ok) {
         tc_fence_after();
         // No visible key: nothing was added, the row is zeros.
         const float rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
         bool finite = true;
-#pragma unroll
-        for (int cb = 0; cb < D; cb += 32) {
+        const uint32_t toa = split ? tmem + L::kColO + lane_base : to;
+#pragma unroll 1
+        for (int cb = cb0; cb < cb1; cb += 32) {
           uint32_t o[32];
-          tmem_ld32(to + cb, o);
+          tmem_ld32(toa + cb, o);
           tmem_wait_ld();
           reg_fence(o);
+          if (split) {
+            uint32_t ob[32];
+            tmem_ld32(toa + L::kStepO + cb, ob);
+            tmem_wait_ld();
+            reg_fence(ob);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), wa, __uint_as_float(ob[i]) * wb));
+          }
           if (mine) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -575,7 +630,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         again_rl = rl;
         again_row = row;
         again_visible = visible;
-        if (mine && p.lse)
+        if (mine && p.lse && (!split || x == 0))
           p.lse[head * p.lse_stride + sq.q0 + row] = visible > 0 ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
       }
     } else if (mine) {

@@ -138,3 +138,26 @@ def test_graph_and_side_stream(adt):
     adt.sage_check()
     assert torch.equal(out, adt.sage_attn_prompt(q, k, v, [0, L]))
     assert not math.isclose(float((out.float() - want.float()).abs().max()), 0.0)
+
+
+@pytest.mark.parametrize("lq,lk,Hq,Hk,D,causal,heads", [
+    ([700, 300], None, 64, 16, 128, True, [0, 3, 33, 63]),             # two waves of pairs, the last ones parted
+    ([600, 90, 1], [2000, 90, 1500], 64, 16, 64, True, [0, 30, 63]),   # long and short pairs mixed
+    ([256], [700], 100, 100, 128, False, [0, 57, 99]),                 # one wave of pairs
+    ([128, 1], [128, 900], 3, 3, 128, True, None),                     # an item alone with one key tile, with several
+    ([64], [640], 5, 1, 64, True, None),
+    ([30], [257], 1, 1, 128, False, None),
+])
+def test_pairs_and_items_alone(adt, lq, lk, Hq, Hk, D, causal, heads):
+    """Row tiles that share a CTA, and row tiles alone whose keys are taken by both halves of one."""
+    lk = lq if lk is None else lk
+    q, k, v = _inputs(lq, lk, Hq, Hk, D, torch.bfloat16, seed=sum(lk) + Hq)
+    cq, ck = _offsets(lq), _offsets(lk)
+    out = torch.full((sum(lq), Hq, D), 9.0, device="cuda", dtype=torch.bfloat16)
+    lse = torch.full((Hq, sum(lq)), 9.0, device="cuda")
+    adt.sage_attn_prompt(q, k, v, cq, ck, out, lse, causal=causal)
+    adt.sage_check()
+    _compare(out, lse, q, k, v, cq, ck, causal, heads=heads)
+    again = torch.empty_like(out)
+    adt.sage_attn_prompt(q, k, v, cq, ck, again, causal=causal)
+    assert torch.equal(out, again)
