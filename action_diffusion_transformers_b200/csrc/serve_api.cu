@@ -22,6 +22,7 @@ using sage_host::device_setup;
 using sage_host::fail;
 using sage_host::launch_check;
 using sage_host::pdl_launch;
+using sage_host::pdl_launch_clusters;
 
 // Token stride of a call's rows (0 means contiguous).
 sage_status check_stride(int64_t stride, int H, int D, const char* name, int64_t* out) {
@@ -136,6 +137,7 @@ TokenWs token_ws(int B, int Hq, int D, int chunks) {
 
 // Shared memory limits of the attention kernels, once per device.
 std::atomic<uint64_t> g_attn_ready{0};
+std::atomic<int> g_clusters[64][4];       // clusters of 2, 4, 8 CTAs ([1], [2], [3]) resident at once, by device
 
 template <class K>
 void attr(cudaError_t* e, K kernel, int bytes) {
@@ -143,7 +145,8 @@ void attr(cudaError_t* e, K kernel, int bytes) {
 }
 template <class E, int D>
 void attn_attr(cudaError_t* e) {
-  attr(e, sage::prompt_attn_kernel<E, D>, sage::PrSmem<D>::kAlloc);
+  attr(e, sage::prompt_attn_kernel<E, D, false>, sage::PrSmem<D>::kAlloc);
+  attr(e, sage::prompt_attn_kernel<E, D, true>, sage::PrSmem<D>::kAlloc);
   attr(e, sage::token_attn_kernel<E, D, 1, sage::kKvInt8>, sage::kTokSmem<D, 1>);
   attr(e, sage::token_attn_kernel<E, D, 1, sage::kKvE4m3>, sage::kTokSmem<D, 1>);
   attr(e, sage::token_attn_kernel<E, D, 2, sage::kKvInt8>, sage::kTokSmem<D, 2>);
@@ -158,6 +161,21 @@ sage_status attn_setup(int dev) {
   attn_attr<sage::Bf16T, 64>(&e);
   attn_attr<sage::Fp16T, 128>(&e);
   attn_attr<sage::Fp16T, 64>(&e);
+  for (int i = 1; i <= 3 && e == cudaSuccess; ++i) {
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = 1u << i;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1u << i);
+    cfg.blockDim = dim3(sage::kPrThreads);
+    cfg.dynamicSmemBytes = sage::PrSmem<128>::kAlloc;
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, sage::prompt_attn_kernel<sage::Bf16T, 128, true>, &cfg);
+    g_clusters[dev][i].store(n);
+  }
   if (e != cudaSuccess) return sage_host::cuda_fail(e, "attention setup");
   g_attn_ready.fetch_or(bit);
   return SAGE_OK;
@@ -304,6 +322,37 @@ int prompt_balance(const sage::PromptParams& p, uint64_t* keys, int n, int lanes
     std::copy(next, next + m, keys);
   }
   return n;
+}
+
+// CTAs per item, its keys dealt out among them: as many as leave all clusters
+// resident (15 of 8 CTAs, 33 of 4, 74 of 2 on a B200) and give each of their
+// tiles two key tiles of the longest item.  The join takes about 4 us, a key tile
+// about 2, so that a few key tiles are left to one CTA: 16 heads x 64 queries over
+// 512 keys 8.9 us alone and about 12 with 2 CTAs, x 128 queries over 1024 keys 18.7
+// and 13.4 with 4.
+int prompt_cluster(const sage::PromptParams& p, int n_seq, int lanes, int dev) {
+  if (p.share) return 1;
+  int64_t items = 0, longest = 0;
+  for (int i = 0; i < n_seq; ++i) {
+    items += (static_cast<int64_t>(p.seq[i].lq) + sage::kPrTile - 1) / sage::kPrTile * lanes;
+    longest = std::max<int64_t>(longest, (static_cast<int64_t>(p.seq[i].lk) + sage::kPrTile - 1) / sage::kPrTile);
+  }
+  int c = 1;
+  for (int i = 1; i <= 3 && items <= g_clusters[dev][i].load() && longest >= 4 << (i - 1); ++i) c = 1 << i;
+  return longest - longest / c >= 4 ? c : 1;
+}
+
+// Every pair parted into its items.
+int prompt_alone(const sage::PromptParams& p, uint64_t* keys, int n) {
+  int m = n;
+  for (int e = 0; e < n; ++e) {
+    const int seq = static_cast<int>(keys[e] >> 24 & 0xFF), pair = static_cast<int>(keys[e] & 0xFFFFF);
+    if (prompt_row_tile(p, 2 * pair + 1) * sage::kPrTile < p.seq[seq].lq)
+      keys[m++] = prompt_key(p, seq, pair, sage::kPrSecond);
+    keys[e] = prompt_key(p, seq, pair, sage::kPrFirst);
+  }
+  std::sort(keys, keys + m, [](uint64_t x, uint64_t y) { return x > y; });
+  return m;
 }
 
 }  // namespace
@@ -583,19 +632,23 @@ sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const 
     if (tiles == 0) continue;
     p.n_seq = m;
     p.sorted = tiles <= sage::kPrMaxOrder ? 1 : 0;
+    p.cluster = p.sorted ? prompt_cluster(p, m, lanes, dev) : 1;
     if (p.sorted) {
       uint64_t keys[sage::kPrMaxOrder];
       for (int i = 0, t = 0; i < m; ++i)
         for (int pair = 0; t < p.tile_end[i]; ++t, ++pair) keys[t] = prompt_key(p, i, pair, sage::kPrBoth);
-      tiles = prompt_balance(p, keys, tiles, lanes, sms);
+      tiles = p.cluster > 1 ? prompt_alone(p, keys, tiles) : prompt_balance(p, keys, tiles, lanes, sms);
       for (int t = 0; t < tiles; ++t) p.order[t] = static_cast<uint32_t>(keys[t]);
     }
-    const dim3 grid(static_cast<unsigned>(tiles * lanes));
+    const dim3 grid(static_cast<unsigned>(tiles * lanes * p.cluster));
     with_flag(a->dtype == SAGE_BF16, [&](auto bf) {
       with_flag(a->D == 128, [&](auto wide) {
         using E = std::conditional_t<bf.value, sage::Bf16T, sage::Fp16T>;
         constexpr int D = wide.value ? 128 : 64;
-        pdl_launch(sage::prompt_attn_kernel<E, D>, grid, sage::kPrThreads, sage::PrSmem<D>::kAlloc, cs, tq, tk, tv, p);
+        with_flag(p.cluster > 1, [&](auto shared) {
+          pdl_launch_clusters(sage::prompt_attn_kernel<E, D, shared.value>, p.cluster, grid, sage::kPrThreads,
+                              sage::PrSmem<D>::kAlloc, cs, tq, tk, tv, p);
+        });
       });
     });
   }

@@ -11,11 +11,21 @@
 // heads running fastest, so that both tiles see about the same keys; where that
 // would leave SMs idle (no more CTAs than SMs with a CTA per two row tiles of one
 // head) the row tiles of one head are paired instead: 144 against 96 CTAs for
-// eight captions x 16 heads, 8.8 against 10.0 us.  An item alone (a pair without
-// its second, or one that the host parts because its end would stand out) gives
-// its even key tiles to A, its odd ones to B, and the two are joined at the end:
-// 1024 tokens x 24 heads 25.7 to 19.4 us, chunks of 32 to 1504 tokens behind up to
-// 3000 earlier ones x 24 heads 112.5 to 104.7.  384 threads:
+// eight captions x 16 heads, 8.8 against 10.0 us.
+//
+// An item alone (a pair without its second, or one that the host parts because its
+// end would stand out) gives its key tiles to A and B in turn, each with a ring of
+// its own, and the two results are joined at the end: 1024 tokens x 24 heads 25.7
+// to 19.4 us, chunks of 32 to 1504 tokens behind up to 3000 earlier ones x 24 heads
+// 112.5 to 100.  (K of A and B loaded before V of either, 3 slots each: in the
+// order K, V of A, K, V of B with 2 slots, A's products held up B's next K; 128
+// queries over 8192 keys took 41 instead of 31 us.)
+// Where the items are few, each is given to a cluster of 2, 4 or 8 CTAs, its key
+// tiles dealt out among all their tiles A and B, and the CTAs' results are joined
+// through distributed shared memory in a fixed order (kCluster): 128 queries over
+// 8192 keys x 16 heads 119 to 31 us, x 4 heads 22, one head of 6000 tokens 88 to 39.
+//
+// 384 threads:
 //   warps 0-3, 4-7  softmax of tile A, of tile B: thread r owns query row r
 //                   (TMEM lane r), reads its 128 scores, writes P back as
 //                   16-bit pairs over the first 64 score columns, 64 keys at a
@@ -64,6 +74,7 @@ template <int D>
 struct PrSmem {
   static constexpr int kTileBytes = kPrTile * D * 2;
   static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kBarSlots = D == 128 ? 6 : 8;          // barriers of slots (see kHalf)
   static constexpr int kQ = 0;                                // A, B
   static constexpr int kRing = 2 * kTileBytes;
   static constexpr int kBar = kRing + kSlots * kTileBytes;
@@ -71,10 +82,19 @@ struct PrSmem {
   static constexpr int kColO = 256, kStepO = D, kColP = kApart ? 384 : 0, kStepP = kApart ? 64 : 128;
   // q[2], s_full[2], pv_done[2], p_full[2][2], s_read[2], full[], empty[], drain[2]
   static constexpr int kQFull = 0, kSFull = 2, kPVDone = 4, kPFull = 6, kSRead = 10, kFull = 12,
-                       kEmpty = kFull + kSlots, kDrain = kEmpty + kSlots, kNumBars = kDrain + 2;
+                       kEmpty = kFull + kBarSlots, kDrain = kEmpty + kBarSlots, kNumBars = kDrain + 2;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kTotal = kMisc + 16;
   static constexpr int kAlloc = kTotal + 1024;
+  // An item alone: each of the two tiles has a ring of its own, of kHalf slots
+  // (D = 128: Q_B's place is one of them).  At the end of a tile's ring, once it
+  // is read, the sums and references of its rows; for a cluster, those of the CTA
+  // at the end of B's, and its O from the start of A's.
+  static constexpr int kHalf = D == 128 ? 3 : 4;
+  static constexpr int kRing2 = kRing + (kSlots - 2 * kHalf) * kTileBytes, kRing2Bytes = kHalf * kTileBytes;
+  static constexpr int kStat = kRing2Bytes - 4096, kStatCta = 2 * kRing2Bytes - 2048;
+  static constexpr int kPartStride = D + 4;                   // floats from row to row of a CTA's O
+  static_assert(kRing2 >= kQ + kTileBytes && kPrTile * kPartStride * 4 <= kStat, "");
 };
 static_assert(PrSmem<128>::kAlloc <= 232448 && PrSmem<64>::kAlloc <= 232448, "shared memory of one CTA");
 
@@ -95,6 +115,7 @@ struct PromptParams {
   int64_t q_stride, k_stride, v_stride, out_stride;
   int64_t lse_stride;       // Tq
   int Hq, G, n_seq, causal;
+  int cluster;              // CTAs that share an item alone, by key tiles: 1, 2, 4, 8
   int share;                // 1: items are paired over the heads of a KV head, 0: over the rows of a head
   float scale_log2;
   int* err;
@@ -216,12 +237,12 @@ __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, volatile
 // only for rows whose first result was not finite though their sum was.
 template <class E, int D>
 __device__ __noinline__ void prompt_row_again(const PromptParams& p, const PromptSeq& sq, int row, int h, int visible,
-                                              float m, float rl) {
+                                              float m, float rl, int d0, int d1) {
   using S = typename E::S;
   const S* q = static_cast<const S*>(p.q) + static_cast<int64_t>(sq.q0 + row) * p.q_stride + static_cast<int64_t>(h) * D;
   const int64_t hk = static_cast<int64_t>(h / p.G) * D;
   S* out = static_cast<S*>(p.out) + static_cast<int64_t>(sq.q0 + row) * p.out_stride + static_cast<int64_t>(h) * D;
-  for (int d = 0; d < D; d += 8) {
+  for (int d = d0; d < d1; d += 8) {
     float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int j = 0; j < visible; ++j) {
       const S* k = static_cast<const S*>(p.k) + static_cast<int64_t>(sq.k0 + j) * p.k_stride + hk;
@@ -253,6 +274,86 @@ __device__ __noinline__ void prompt_row_again(const PromptParams& p, const Promp
   }
 }
 
+// All threads of all CTAs of the cluster.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(addr), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ float2 peer_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_ld4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// Where a CTA of a cluster leaves its sums and references, and its O.
+template <int D>
+__device__ __forceinline__ float2* prompt_stat(uint8_t* smem) {
+  return reinterpret_cast<float2*>(smem + PrSmem<D>::kRing2 + PrSmem<D>::kStatCta);
+}
+template <int D>
+__device__ __forceinline__ float* prompt_part(uint8_t* smem) {
+  return reinterpret_cast<float*>(smem + PrSmem<D>::kRing2);
+}
+
+// O = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over the CTAs c of the cluster,
+// in their order; each CTA takes a share of the rows, a thread 8 channels.
+template <class E, int D>
+__device__ __forceinline__ void prompt_join(const PromptParams& p, const PromptSeq& sq, uint8_t* smem, int rank, int row0,
+                                            int head, int off) {
+  using S = typename E::S;
+  constexpr int kPieces = D / 8;
+  const float kNegInf = -__int_as_float(0x7F800000);
+  const int share = kPrTile / p.cluster;
+  for (int i = threadIdx.x; i < share * kPieces; i += kPrThreads) {
+    const int r = rank * share + i / kPieces, d = (i % kPieces) * 8, row = row0 + r;
+    if (row >= sq.lq) continue;
+    const uint32_t stat = smem_u32(prompt_stat<D>(smem) + r);
+    const uint32_t part = smem_u32(prompt_part<D>(smem) + r * PrSmem<D>::kPartStride + d);
+    float m = kNegInf, l = 0.f;
+    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < p.cluster; ++c) m = fmaxf(m, peer_ld2(peer_addr(stat, c)).x);
+    for (int c = 0; c < p.cluster; ++c) {
+      const float2 st = peer_ld2(peer_addr(stat, c));
+      const float w = st.x == kNegInf ? 0.f : ex2_approx(st.x - m);
+      const uint32_t at = peer_addr(part, c);
+      const float4 a = peer_ld4(at), b = peer_ld4(at + 16);
+      l = fmaf(st.y, w, l);
+      const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = fmaf(f[k], w, o[k]);
+    }
+    const int visible = p.causal ? min(sq.lk, max(0, row + off + 1)) : sq.lk;
+    const float rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      finite = finite && fabsf(o[k]) < __int_as_float(0x7F800000);
+      o[k] *= rl;
+    }
+    if (finite || !(fabsf(l) < __int_as_float(0x7F800000))) {
+      Piece<E, 8> pc;
+      pc.put(o);
+      pc.store(static_cast<S*>(p.out) + static_cast<int64_t>(sq.q0 + row) * p.out_stride +
+               static_cast<int64_t>(head) * D + d);
+    } else {
+      prompt_row_again<E, D>(p, sq, row, head, visible, m == kNegInf ? 0.f : m, rl, d, d + 8);
+    }
+    if (p.lse && d == 0)
+      p.lse[head * p.lse_stride + sq.q0 + row] = visible > 0 ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+  }
+}
+
 // The launch gives each of the 384 threads 168 registers; the last four warps
 // hand most of theirs to the softmax warps: 2 x 224 + 56 = 3 x 168.
 constexpr int kPrRegsSoftmax = 224, kPrRegsOther = 56;
@@ -266,13 +367,13 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-template <class E, int D>
+template <class E, int D, bool kCluster>
 __global__ void __launch_bounds__(kPrThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PromptParams p) {
   using L = PrSmem<D>;
   using S = typename E::S;
-  constexpr int kSlots = L::kSlots, kHalf = kSlots / 2;
+  constexpr int kSlots = L::kSlots, kHalf = L::kHalf;
   constexpr bool kBf16 = std::is_same<E, Bf16T>::value;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -286,8 +387,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   // with the most key tiles come first: sorted by the host, or, where they are
   // many, the sequences by length and each from its end to its start.
   const int lanes = p.share ? p.Hq / p.G : p.Hq;
-  const int tile = blockIdx.x / lanes;
-  const int hb = blockIdx.x - tile * lanes;
+  const int cluster = kCluster ? p.cluster : 1;
+  const int cta = blockIdx.x / cluster, rank = blockIdx.x - cta * cluster;
+  const int tile = cta / lanes;
+  const int hb = cta - tile * lanes;
   int lo = 0, pair;
   uint32_t which = kPrBoth;
   if (p.sorted) {
@@ -322,17 +425,21 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const int seen = p.causal ? min(sq.lk, last + off + 1) : sq.lk;
     nt[x] = seen > 0 ? (seen + kPrTile - 1) / kPrTile : 0;
   }
-  const int n = max(nt[0], nt[1]);
-  // An item alone: tile A takes its even key tiles, tile B the odd ones, each
-  // with half of the ring, and the two are joined at the end.
-  const bool split = alone && n > 1;
+  int n = max(nt[0], nt[1]);                              // key tiles that this CTA loads
+  // An item alone: its key tiles go round the tiles A and B of its CTAs, each with
+  // half of the ring, and the results are joined at the end.
+  const int stride = 2 * cluster;
+  const bool split = kCluster || (alone && n > 1);
   if (split) {
-    nt[0] = (n + 1) / 2;
-    nt[1] = n / 2;
+    const int all = n;
+    for (int x = 0; x < 2; ++x) nt[x] = max(0, (all - 2 * rank - x + stride - 1) / stride);
+    n = nt[0] + nt[1];
   } else if (alone) {
     nt[1] = 0;
     rows[1] = sq.lq;                                    // no rows
   }
+
+  const int ring = split ? L::kRing2 : L::kRing;
 
   if (warp == kPrWarpMma) {
     tmem_alloc(tmem_slot, 512);
@@ -373,13 +480,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       };
       uint32_t issued = 0, parity = 0;                  // bit per slot: loaded, parity of its last load
       for (int it = 0; it < 2 * n; ++it) {
-        // Split: loads 0, 1, 4, 5, ... are tile A's, its own loads 0, 1, 2, 3, ...
-        const int own = split ? (it >> 2) * 2 + (it & 1) : it;
-        const int slot = split ? ((it >> 1) & 1) * kHalf + own % kHalf : own % kSlots;
+        // Split: K of A and B, V of A and B, ... (the last round may be A's alone).
+        const bool one = split && (it >> 2) >= nt[1];
+        const int x = !split || one ? 0 : it & 1, kv = !split || one ? it & 1 : (it >> 1) & 1;
+        const int own = split ? (it >> 2) * 2 + kv : it;
+        const int slot = split ? x * kHalf + own % kHalf : own % kSlots;
         const uint32_t use = static_cast<uint32_t>(split ? own / kHalf : own / kSlots);
         if (it == 0 && nt[0] > 0) load(smem + L::kQ, &tm_q, heads[0], sq.q0 + rows[0], &bars[L::kQFull]);
         if (use > 0 && !mbar_wait_bounded(&bars[L::kEmpty + slot], (use - 1) & 1, abort_flag, tmo)) break;
-        load(smem + L::kRing + slot * L::kTileBytes, (it & 1) ? &tm_v : &tm_k, hk, sq.k0 + (it >> 1) * kPrTile,
+        const int j = split ? (it >> 2) * stride + 2 * rank + x : it >> 1;
+        load(smem + ring + slot * L::kTileBytes, kv ? &tm_v : &tm_k, hk, sq.k0 + j * kPrTile,
              &bars[L::kFull + slot]);
         issued |= 1u << slot;
         parity = (parity & ~(1u << slot)) | (use & 1) << slot;
@@ -393,16 +503,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         volatile int* nf = reinterpret_cast<volatile int*>(&none);
         if (nt[0] > 0) mbar_wait_bounded(&bars[L::kQFull], 0, nf, drain);
         if (nt[1] > 0 && !split) mbar_wait_bounded(&bars[L::kQFull + 1], 0, nf, drain);
-        for (int slot = 0; slot < kSlots; ++slot)
+        for (int slot = 0; slot < L::kBarSlots; ++slot)
           if (issued >> slot & 1) mbar_wait_bounded(&bars[L::kFull + slot], parity >> slot & 1, nf, drain);
       }
     }
    } else if (warp < kPrWarpLoad) {
     // ------------------------------------------------------------ MMA of tile A, of tile B
-    if (lane == 0 && n > 0) {
-      const int x = warp - kPrWarpMma;
-      const int ntx = x ? nt[1] : nt[0];
-      const int steps = split ? ntx : n;              // key tiles whose slots this tile gives back
+    const int x = warp - kPrWarpMma;
+    const int ntx = x ? nt[1] : nt[0];
+    const int steps = split ? ntx : n;                // key tiles whose slots this tile gives back
+    if (lane == 0 && steps > 0) {
       const int qx = split ? 0 : x;
       constexpr uint32_t kFmt = kBf16 ? 1u : 0u;
       constexpr uint32_t kIdescQK = make_idesc(1u, kFmt, 128u, 128u);
@@ -414,7 +524,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       auto wait_full = [&](int it) { return wait(L::kFull + slot_of(it), split ? it / kHalf : it / kSlots); };
       auto scores = [&](int j) {                  // S_x(j) = Q_x K_j^T
         const uint64_t qd = make_sdesc(smem_u32(smem + L::kQ + qx * L::kTileBytes), 1024u, 2u);
-        const uint64_t kd = make_sdesc(smem_u32(smem + L::kRing + slot_of(2 * j) * L::kTileBytes), 1024u, 2u);
+        const uint64_t kd = make_sdesc(smem_u32(smem + ring + slot_of(2 * j) * L::kTileBytes), 1024u, 2u);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t step = (kk & 3) * 2 + (kk >> 2) * (kPrTile * 128 / 16);
@@ -424,7 +534,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       };
       auto products = [&](int j) {                // O_x += P_x(j) V_j, as its halves come in
         const uint64_t vd =
-            make_sdesc_mn(smem_u32(smem + L::kRing + slot_of(2 * j + 1) * L::kTileBytes), kPrTile * 128);
+            make_sdesc_mn(smem_u32(smem + ring + slot_of(2 * j + 1) * L::kTileBytes), kPrTile * 128);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!wait(L::kPFull + 2 * x + half, j)) return false;
@@ -509,7 +619,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[L::kSRead + x]);
       }
-      const int valid = visible - (split ? 2 * j + x : j) * kPrTile;
+      const int valid = visible - (split ? j * stride + 2 * rank + x : j) * kPrTile;
       const bool masked = __any_sync(0xFFFFFFFFu, valid < kPrTile);
       if (masked) {
 #pragma unroll
@@ -567,20 +677,20 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     const bool mine = row < sq.lq;                 // also false for a tile without an item
     S* dst = static_cast<S*>(p.out) + static_cast<int64_t>(sq.q0 + row) * p.out_stride + static_cast<int64_t>(head) * D;
-    if (ntx > 0) {
-      if (ok) ok = pr_wait(&bars[L::kPVDone + x], static_cast<uint32_t>(ntx - 1) & 1, abort_flag, tmo);
+    if (split || ntx > 0) {
+      if (ok && ntx > 0) ok = pr_wait(&bars[L::kPVDone + x], static_cast<uint32_t>(ntx - 1) & 1, abort_flag, tmo);
       int cb0 = 0, cb1 = D;                              // channels that this thread stores
       float wa = 1.f, wb = 0.f;                          // split: weights of O_A, O_B
       if (split) {
         // O = (2^(m_A - m) O_A + 2^(m_B - m) O_B) / l, l alike, m the larger of the
         // two: thread r of tile A takes the first half of the channels of row r, of
         // tile B the second; both reach that TMEM lane.  Every softmax warp comes
-        // here, after a wait that ran out too.  Q_B's place is free.
-        float2* stat = reinterpret_cast<float2*>(smem + L::kQ + L::kTileBytes);
-        stat[x * kPrTile + r] = make_float2(m, l);
+        // here, after a wait that ran out too.
+        float2* stat = reinterpret_cast<float2*>(smem + L::kRing2 + L::kStat);
+        stat[x * (L::kRing2Bytes / 8) + r] = make_float2(m, l);
         tc_fence_before();
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        const float2 a = stat[r], b = stat[kPrTile + r];
+        const float2 a = stat[r], b = stat[L::kRing2Bytes / 8 + r];
         m = fmaxf(a.x, b.x);
         wa = a.x == kNegInf ? 0.f : ex2_approx(a.x - m);
         wb = b.x == kNegInf ? 0.f : ex2_approx(b.x - m);
@@ -588,7 +698,33 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         cb0 = x * (D / 2);
         cb1 = cb0 + D / 2;
       }
-      if (ok) {
+      if (kCluster && ok) {
+        // For the join of the cluster: sum, reference and O of this CTA's keys to
+        // shared memory (the ring is read: both tiles' products are done).
+        tc_fence_after();
+        if (x == 0) prompt_stat<D>(smem)[r] = make_float2(m, l);
+        float* o = prompt_part<D>(smem) + r * L::kPartStride;
+#pragma unroll 1
+        for (int cb = cb0; cb < cb1; cb += 16) {
+          float f[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] = 0.f;
+          for (int y = 0; y < 2; ++y) {
+            if (nt[y] > 0) {                             // or O was never written
+              uint32_t t[16];
+              tmem_ld16(tmem + L::kColO + y * L::kStepO + lane_base + cb, t);
+              tmem_wait_ld();
+              reg_fence16(t);
+              const float w = y ? wb : wa;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) f[i] = fmaf(__uint_as_float(t[i]), w, f[i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(o + cb + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+        }
+      } else if (ok) {
         tc_fence_after();
         // No visible key: nothing was added, the row is zeros.
         const float rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
@@ -650,7 +786,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (again) prompt_row_again<E, D>(p, sq, again_row, (warp >> 2) ? heads[1] : heads[0], again_visible, again_m, again_rl);
+  if constexpr (kCluster) {
+    // Every CTA of the cluster comes here, after a wait that ran out too.
+    __syncwarp();
+    cluster_sync();
+    prompt_join<E, D>(p, sq, smem, rank, rows[0], heads[0], off);
+    cluster_sync();                                      // nobody leaves while its part is read
+    return;
+  }
+  if (again) prompt_row_again<E, D>(p, sq, again_row, (warp >> 2) ? heads[1] : heads[0], again_visible, again_m, again_rl, 0,
+                                   D);
 }
 
 }  // namespace sage

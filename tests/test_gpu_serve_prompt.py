@@ -161,3 +161,43 @@ def test_pairs_and_items_alone(adt, lq, lk, Hq, Hk, D, causal, heads):
     again = torch.empty_like(out)
     adt.sage_attn_prompt(q, k, v, cq, ck, again, causal=causal)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lq,lk,Hq,Hk,D,causal", [
+    ([1], [5000], 4, 2, 128, True),                        # 8 CTAs per row tile
+    ([100, 3], [4096, 130], 4, 4, 64, True),               # a sequence with fewer key tiles than CTAs
+    ([257], [4000], 3, 1, 128, False),
+    ([128], [2049], 16, 8, 64, True),
+    ([300, 20], [1300, 0], 8, 2, 128, True),               # 4; rows without any key
+    ([1000], [700], 2, 2, 64, True),                       # rows without any key beside rows with some
+    ([640], [640], 13, 13, 128, True),                     # 2
+])
+def test_row_tiles_shared_by_a_cluster(adt, dtype, lq, lk, Hq, Hk, D, causal):
+    """Few row tiles over many keys: several CTAs take the keys of one and join what they found."""
+    q, k, v = _inputs(lq, lk, Hq, Hk, D, dtype, seed=sum(lk) + D)
+    cq, ck = _offsets(lq), _offsets(lk)
+    out = torch.full((sum(lq), Hq, D), 9.0, device="cuda").to(dtype)
+    lse = torch.full((Hq, sum(lq)), 9.0, device="cuda")
+    adt.sage_attn_prompt(q, k, v, cq, ck, out, lse, causal=causal)
+    adt.sage_check()
+    _compare(out, lse, q, k, v, cq, ck, causal)
+    again = torch.empty_like(out)
+    adt.sage_attn_prompt(q, k, v, cq, ck, again, causal=causal)
+    assert torch.equal(out, again)
+
+
+def test_what_masked_places_hold_does_not_matter_to_a_cluster(adt):
+    Lq, Lk, D = 60, 3000, 128
+    q, k, v = _inputs([Lq], [Lk], 2, 1, D, torch.bfloat16, seed=21)
+    clean = adt.sage_attn_prompt(q, k, v, [0, Lq], [0, Lk])
+    k2, v2 = k.clone(), v.clone()
+    k2[Lk - 20:], v2[Lk - 20:] = float("nan"), float("inf")         # seen by the last 20 rows alone
+    v2[7, :, 5] = float("-inf")                                     # one channel of one token, seen by all
+    got = adt.sage_attn_prompt(q, k2, v2, [0, Lq], [0, Lk])
+    adt.sage_check()
+    rest = [c for c in range(D) if c != 5]
+    a, b = got[:40][..., rest].double(), clean[:40][..., rest].double()
+    lim = 2 * torch.finfo(torch.bfloat16).eps * b.abs() + 4 * torch.finfo(torch.bfloat16).eps
+    assert bool(((a - b).abs() <= lim).all())
+    assert bool(torch.isinf(got[:40, :, 5]).all()) and bool(torch.isnan(got[40:]).all())
