@@ -26,8 +26,12 @@
 // channels above 2^-14 of the largest keep every bit, the others are off by at
 // most 2^-25 of it.  P carries the V scale of its key and a power of two per
 // head that keeps the largest weight met so far near 1, so its rounding to f16
-// (2^-11 relative) is never an underflow of weights that matter.  Sums, row
-// maxima and the output stay in 32 bits.
+// (2^-11 relative) is never an underflow of weights that matter.  That rounding is
+// far below a bf16 output's own (2^-8), but equal to an fp16 output's: there P goes
+// in as two f16 parts (kFine), what the first leaves out being the second, which
+// takes the error against 64 bits from 1.4 times that of the output's rounding to
+// 1.0 times, for 2% of the time (64 sequences of 300 to 8192 keys 102.8 to 105.1
+// us; INT8 codes 107 to 112).  Sums, row maxima and the output stay in 32 bits.
 //
 // A CTA takes one chunk of keys of one segment (a sequence and a KV head with up
 // to 8 * NT of its query heads); its warps take 32-key tiles in turn and are
@@ -197,7 +201,7 @@ struct TokState {
 
 // n: keys of the tile that exist; have: bit h is set where the page of half h
 // does.  What lies in the other places may be anything: none of it takes part.
-template <int D, int NT, int kFmt>
+template <int D, int NT, int kFmt, bool kFine>
 __device__ __forceinline__ void tok_step(const uint8_t* stage, int n, int have, const uint32_t (&q)[NT][D / 16][2],
                                          const float (&qf)[NT][2], TokState<D, NT>& st, int lane) {
   using Q = TokQueue<D>;
@@ -246,7 +250,7 @@ __device__ __forceinline__ void tok_step(const uint8_t* stage, int n, int have, 
       in[h][r] = all || (16 * h + 8 * r + g < n && ((have >> h) & 1));
       if (!in[h][r]) vs[h][r] = 0.f;
     }
-  uint32_t pb[NT][2][2];
+  uint32_t pb[NT][2][2], pl[NT][2][2];         // P in f16; kFine: what that rounding left out, in f16
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
     // s[b][h]: (key g, heads 2t, 2t+1), (key g + 8, the same heads)
@@ -313,8 +317,13 @@ __device__ __forceinline__ void tok_step(const uint8_t* stage, int n, int have, 
     st.l[b][1] += (e[0][1] + e[0][3]) + (e[1][1] + e[1][3]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      pb[b][h][0] = movmatrix_trans(f16x2_pack(w[h][0], w[h][1]));
-      pb[b][h][1] = movmatrix_trans(f16x2_pack(w[h][2], w[h][3]));
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t pk = f16x2_pack(w[h][2 * r], w[h][2 * r + 1]);
+        pb[b][h][r] = movmatrix_trans(pk);
+        if constexpr (kFine)
+          pl[b][h][r] = movmatrix_trans(f16x2_pack(w[h][2 * r] - Fp16T::lo(pk), w[h][2 * r + 1] - Fp16T::hi(pk)));
+      }
     }
   }
 #pragma unroll
@@ -356,7 +365,10 @@ __device__ __forceinline__ void tok_step(const uint8_t* stage, int n, int have, 
         codes_f16<kFmt>(c ? hi01 : lo01, a[0], a[1]);
         codes_f16<kFmt>(c ? hi23 : lo23, a[2], a[3]);
 #pragma unroll
-        for (int b = 0; b < NT; ++b) mma_f16_16816(st.o[b][2 * i + c], a, pb[b][h][0], pb[b][h][1]);
+        for (int b = 0; b < NT; ++b) {
+          mma_f16_16816(st.o[b][2 * i + c], a, pb[b][h][0], pb[b][h][1]);
+          if constexpr (kFine) mma_f16_16816(st.o[b][2 * i + c], a, pl[b][h][0], pl[b][h][1]);
+        }
       }
     }
   }
@@ -473,7 +485,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
       cp_async_wait<1>();
       __syncwarp();        // the other lanes' copies too
       if (have)
-        tok_step<D, NT, kFmt>(queue + stage * Q::kStage, len - tile * kTokTile, have, q, qf, st, lane);
+        tok_step<D, NT, kFmt, std::is_same<E, Fp16T>::value>(queue + stage * Q::kStage, len - tile * kTokTile, have, q, qf, st, lane);
       have = then;
       __syncwarp();        // the stage is free
     }
