@@ -201,3 +201,35 @@ def test_what_masked_places_hold_does_not_matter_to_a_cluster(adt):
     lim = 2 * torch.finfo(torch.bfloat16).eps * b.abs() + 4 * torch.finfo(torch.bfloat16).eps
     assert bool(((a - b).abs() <= lim).all())
     assert bool(torch.isinf(got[:40, :, 5]).all()) and bool(torch.isnan(got[40:]).all())
+
+
+def test_more_pairs_than_are_sorted(adt):
+    lens = [1 + (53 * i) % 290 for i in range(150)]
+    past = [(31 * i) % 70 for i in range(150)]
+    lk = [a + b for a, b in zip(lens, past)]
+    cq, ck = _offsets(lens), _offsets(lk)
+    q, k, v = _inputs(lens, lk, 9, 1, 64, torch.bfloat16, seed=31)
+    lse = torch.empty(9, cq[-1], device="cuda")
+    out = adt.sage_attn_prompt(q, k, v, cq, ck, lse=lse)
+    adt.sage_check()
+    _compare(out, lse, q, k, v, cq, ck, True, heads=[0, 8])
+
+
+def test_graph_with_clusters_beside_an_eager_call(adt):
+    Lq, Lk, D = 100, 3000, 128
+    q, k, v = _inputs([Lq], [Lk], 4, 2, D, torch.float16, seed=33)
+    cu = [0, Lq], [0, Lk]
+    want = adt.sage_attn_prompt(q, k, v, *cu)
+    out = torch.zeros_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        adt.sage_attn_prompt(q, k, v, *cu, out=out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = torch.empty_like(want)
+    for _ in range(3):
+        graph.replay()
+        adt.sage_attn_prompt(q, k, v, *cu, out=other, stream=side)
+    torch.cuda.synchronize()
+    adt.sage_check()
+    assert torch.equal(out, want) and torch.equal(other, want)
