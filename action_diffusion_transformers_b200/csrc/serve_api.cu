@@ -137,7 +137,7 @@ TokenWs token_ws(int B, int Hq, int D, int chunks) {
 
 // Shared memory limits of the attention kernels, once per device.
 std::atomic<uint64_t> g_attn_ready{0};
-std::atomic<int> g_clusters[64][4];       // clusters of 2, 4, 8 CTAs ([1], [2], [3]) resident at once, by device
+std::atomic<int> g_clusters[64][sage::kPrMaxCluster + 1];   // clusters of so many CTAs resident at once, by device
 
 template <class K>
 void attr(cudaError_t* e, K kernel, int bytes) {
@@ -161,20 +161,20 @@ sage_status attn_setup(int dev) {
   attn_attr<sage::Bf16T, 64>(&e);
   attn_attr<sage::Fp16T, 128>(&e);
   attn_attr<sage::Fp16T, 64>(&e);
-  for (int i = 1; i <= 3 && e == cudaSuccess; ++i) {
+  for (int c = 2; c <= sage::kPrMaxCluster && e == cudaSuccess; ++c) {
     cudaLaunchAttribute a;
     a.id = cudaLaunchAttributeClusterDimension;
-    a.val.clusterDim.x = 1u << i;
+    a.val.clusterDim.x = static_cast<unsigned>(c);
     a.val.clusterDim.y = a.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1u << i);
+    cfg.gridDim = dim3(static_cast<unsigned>(c));
     cfg.blockDim = dim3(sage::kPrThreads);
     cfg.dynamicSmemBytes = sage::PrSmem<128>::kAlloc;
     cfg.attrs = &a;
     cfg.numAttrs = 1;
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, sage::prompt_attn_kernel<sage::Bf16T, 128, true>, &cfg);
-    g_clusters[dev][i].store(n);
+    g_clusters[dev][c].store(n);
   }
   if (e != cudaSuccess) return sage_host::cuda_fail(e, "attention setup");
   g_attn_ready.fetch_or(bit);
@@ -324,12 +324,12 @@ int prompt_balance(const sage::PromptParams& p, uint64_t* keys, int n, int lanes
   return n;
 }
 
-// CTAs per item, its keys dealt out among them: as many as leave all clusters
-// resident (15 of 8 CTAs, 33 of 4, 74 of 2 on a B200) and give each of their
-// tiles two key tiles of the longest item.  The join takes about 4 us, a key tile
-// about 2, so that a few key tiles are left to one CTA: 16 heads x 64 queries over
-// 512 keys 8.9 us alone and about 12 with 2 CTAs, x 128 queries over 1024 keys 18.7
-// and 13.4 with 4.
+// CTAs per item, its keys dealt out among them: the fewest of those whose clusters
+// are all resident (15 of 8 CTAs, 33 of 4, 74 of 2 on a B200) that leave the longest
+// item the fewest steps, if that saves three, what the join takes (600 tokens x 8
+// heads 11.1 us alone and 13.3 in clusters, 128 queries over 1024 keys x 16 heads
+// 18.7 and 13.4).
+constexpr int kPrJoinSteps = 3;
 int prompt_cluster(const sage::PromptParams& p, int n_seq, int lanes, int dev) {
   if (p.share) return 1;
   int64_t items = 0, longest = 0;
@@ -337,9 +337,11 @@ int prompt_cluster(const sage::PromptParams& p, int n_seq, int lanes, int dev) {
     items += (static_cast<int64_t>(p.seq[i].lq) + sage::kPrTile - 1) / sage::kPrTile * lanes;
     longest = std::max<int64_t>(longest, (static_cast<int64_t>(p.seq[i].lk) + sage::kPrTile - 1) / sage::kPrTile);
   }
-  int c = 1;
-  for (int i = 1; i <= 3 && items <= g_clusters[dev][i].load() && longest >= 4 << (i - 1); ++i) c = 1 << i;
-  return longest - longest / c >= 4 ? c : 1;
+  auto steps = [&](int c) { return (longest + 2 * c - 1) / (2 * c); };
+  int best = 1;
+  for (int c = 2; c <= sage::kPrMaxCluster; ++c)
+    if (items <= g_clusters[dev][c].load() && steps(c) < steps(best)) best = c;
+  return steps(1) - steps(best) >= kPrJoinSteps ? best : 1;
 }
 
 // Every pair parted into its items.

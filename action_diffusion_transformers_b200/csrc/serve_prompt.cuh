@@ -20,7 +20,7 @@
 // 112.5 to 100.  (K of A and B loaded before V of either, 3 slots each: in the
 // order K, V of A, K, V of B with 2 slots, A's products held up B's next K; 128
 // queries over 8192 keys took 41 instead of 31 us.)
-// Where the items are few, each is given to a cluster of 2, 4 or 8 CTAs, its key
+// Where the items are few, each is given to a cluster of 2 to 8 CTAs, its key
 // tiles dealt out among all their tiles A and B, and the CTAs' results are joined
 // through distributed shared memory in a fixed order (kCluster): 128 queries over
 // 8192 keys x 16 heads 119 to 31 us, x 4 heads 22, one head of 6000 tokens 88 to 39.
@@ -67,6 +67,7 @@ constexpr int kPrTile = 128;
 constexpr int kPrThreads = 384;          // 2 x 4 softmax warps, two for MMA, one for loads, one idle
 constexpr int kPrWarpMma = 8, kPrWarpLoad = 10;
 constexpr int kPrMaxSeq = 256;          // sequences per launch
+constexpr int kPrMaxCluster = 8;         // CTAs that share an item at most
 constexpr int kPrMaxOrder = 512;        // pairs up to which the host sorts them
 constexpr float kPrRaise = 8.f;
 
@@ -115,7 +116,7 @@ struct PromptParams {
   int64_t q_stride, k_stride, v_stride, out_stride;
   int64_t lse_stride;       // Tq
   int Hq, G, n_seq, causal;
-  int cluster;              // CTAs that share an item alone, by key tiles: 1, 2, 4, 8
+  int cluster;              // CTAs that share an item alone, by key tiles: 1 .. kPrMaxCluster
   int share;                // 1: items are paired over the heads of a KV head, 0: over the rows of a head
   float scale_log2;
   int* err;
@@ -274,7 +275,7 @@ __device__ __noinline__ void prompt_row_again(const PromptParams& p, const Promp
   }
 }
 
-// All threads of all CTAs of the cluster.
+// All threads of all CTAs of the cluster, each warp whole.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -307,31 +308,49 @@ __device__ __forceinline__ float* prompt_part(uint8_t* smem) {
 }
 
 // O = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over the CTAs c of the cluster,
-// in their order; each CTA takes a share of the rows, a thread 8 channels.
+// in their order; each CTA takes a share of the rows, a thread 8 channels.  For the
+// softmax warps: the others have given their registers away.
 template <class E, int D>
 __device__ __forceinline__ void prompt_join(const PromptParams& p, const PromptSeq& sq, uint8_t* smem, int rank, int row0,
                                             int head, int off) {
   using S = typename E::S;
   constexpr int kPieces = D / 8;
   const float kNegInf = -__int_as_float(0x7F800000);
-  const int share = kPrTile / p.cluster;
-  for (int i = threadIdx.x; i < share * kPieces; i += kPrThreads) {
+  const int share = (kPrTile + p.cluster - 1) / p.cluster;
+  for (int i = threadIdx.x; i < share * kPieces; i += 32 * kPrWarpMma) {
     const int r = rank * share + i / kPieces, d = (i % kPieces) * 8, row = row0 + r;
-    if (row >= sq.lq) continue;
+    if (r >= kPrTile || row >= sq.lq) continue;
     const uint32_t stat = smem_u32(prompt_stat<D>(smem) + r);
     const uint32_t part = smem_u32(prompt_part<D>(smem) + r * PrSmem<D>::kPartStride + d);
     float m = kNegInf, l = 0.f;
     float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int c = 0; c < p.cluster; ++c) m = fmaxf(m, peer_ld2(peer_addr(stat, c)).x);
-    for (int c = 0; c < p.cluster; ++c) {
-      const float2 st = peer_ld2(peer_addr(stat, c));
-      const float w = st.x == kNegInf ? 0.f : ex2_approx(st.x - m);
-      const uint32_t at = peer_addr(part, c);
-      const float4 a = peer_ld4(at), b = peer_ld4(at + 16);
-      l = fmaf(st.y, w, l);
-      const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float2 st[kPrMaxCluster];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = fmaf(f[k], w, o[k]);
+    for (int c = 0; c < kPrMaxCluster; ++c) st[c] = c < p.cluster ? peer_ld2(peer_addr(stat, c)) : make_float2(kNegInf, 0.f);
+#pragma unroll
+    for (int c = 0; c < kPrMaxCluster; ++c) m = fmaxf(m, st[c].x);
+#pragma unroll
+    for (int c0 = 0; c0 < kPrMaxCluster; c0 += 4) {
+      float4 part4[4][2];                                // four peers' pieces under way
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c0 + c < p.cluster) {
+          const uint32_t at = peer_addr(part, c0 + c);
+          part4[c][0] = peer_ld4(at);
+          part4[c][1] = peer_ld4(at + 16);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c0 + c < p.cluster) {
+          const float w = st[c0 + c].x == kNegInf ? 0.f : ex2_approx(st[c0 + c].x - m);
+          const float4 a = part4[c][0], b = part4[c][1];
+          const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          l = fmaf(st[c0 + c].y, w, l);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] = fmaf(f[k], w, o[k]);
+        }
+      }
     }
     const int visible = p.causal ? min(sq.lk, max(0, row + off + 1)) : sq.lk;
     const float rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
@@ -587,6 +606,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       mbar_wait_bounded(&bars[L::kDrain + x], 0, reinterpret_cast<volatile int*>(&none), 200000000);
     }
    }
+   if constexpr (kCluster) {
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
+   }
   } else {
     // ------------------------------------------------------------ softmax
     regs_inc<kPrRegsSoftmax>();
@@ -776,6 +800,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       for (int d = 0; d < D; d += 8) z.store(dst + d);
       if (p.lse) p.lse[head * p.lse_stride + sq.q0 + row] = kNegInf;
     }
+    if constexpr (kCluster) {
+      // Every warp of the cluster meets twice, after a wait that ran out too: the
+      // CTAs' parts are written, and nobody leaves while they are read.
+      __syncwarp();
+      cluster_sync();
+      prompt_join<E, D>(p, sq, smem, rank, rows[0], heads[0], off);
+      __syncwarp();
+      cluster_sync();
+    }
   }
 
   __syncwarp();
@@ -785,14 +818,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   if (warp == kPrWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
-  }
-  if constexpr (kCluster) {
-    // Every CTA of the cluster comes here, after a wait that ran out too.
-    __syncwarp();
-    cluster_sync();
-    prompt_join<E, D>(p, sq, smem, rank, rows[0], heads[0], off);
-    cluster_sync();                                      // nobody leaves while its part is read
-    return;
   }
   if (again) prompt_row_again<E, D>(p, sq, again_row, (warp >> 2) ? heads[1] : heads[0], again_visible, again_m, again_rl, 0,
                                    D);
