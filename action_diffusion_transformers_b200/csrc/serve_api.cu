@@ -326,9 +326,9 @@ int prompt_balance(const sage::PromptParams& p, uint64_t* keys, int n, int lanes
 
 // CTAs per item, its keys dealt out among them: the fewest of those whose clusters
 // are all resident (15 of 8 CTAs, 33 of 4, 74 of 2 on a B200) that leave the longest
-// item the fewest steps, if that saves three, what the join takes (600 tokens x 8
-// heads 11.1 us alone and 13.3 in clusters, 128 queries over 1024 keys x 16 heads
-// 18.7 and 13.4).
+// item the fewest steps, if that saves three, about what the join takes (600 tokens
+// x 8 heads 10.9 us alone and 13.3 in clusters, 128 queries over 1024 keys x 16
+// heads 18.7 and 12.0).
 constexpr int kPrJoinSteps = 3;
 int prompt_cluster(const sage::PromptParams& p, int n_seq, int lanes, int dev) {
   if (p.share) return 1;

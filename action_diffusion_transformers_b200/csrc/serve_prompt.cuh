@@ -17,13 +17,15 @@
 // end would stand out) gives its key tiles to A and B in turn, each with a ring of
 // its own, and the two results are joined at the end: 1024 tokens x 24 heads 25.7
 // to 19.4 us, chunks of 32 to 1504 tokens behind up to 3000 earlier ones x 24 heads
-// 112.5 to 100.  (K of A and B loaded before V of either, 3 slots each: in the
+// 112.5 to 98.  (K of A and B loaded before V of either, 3 slots each: in the
 // order K, V of A, K, V of B with 2 slots, A's products held up B's next K; 128
 // queries over 8192 keys took 41 instead of 31 us.)
 // Where the items are few, each is given to a cluster of 2 to 8 CTAs, its key
 // tiles dealt out among all their tiles A and B, and the CTAs' results are joined
 // through distributed shared memory in a fixed order (kCluster): 128 queries over
-// 8192 keys x 16 heads 119 to 31 us, x 4 heads 22, one head of 6000 tokens 88 to 39.
+// 8192 keys x 16 heads 119 to 27 us, x 4 heads 21, one head of 6000 tokens 88 to 38.
+// (The join is the softmax warps' own: behind the point where all warps meet, the
+// compiler keeps to the 56 registers of the others, and the chunk took 30 us.)
 //
 // 384 threads:
 //   warps 0-3, 4-7  softmax of tile A, of tile B: thread r owns query row r
@@ -484,9 +486,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   // the kernel before.
   pdl_enter();
 
-  bool again = false;                      // this thread's row has to be computed once more
-  float again_m = 0.f, again_rl = 0.f;
-  int again_row = 0, again_visible = 0;
   if (warp >= kPrWarpMma) {
    regs_dec<kPrRegsOther>();
    if (warp == kPrWarpLoad) {
@@ -628,7 +627,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const int visible = p.causal ? min(sq.lk, max(0, row + off + 1)) : sq.lk;
     float m = kNegInf;                             // reference, log2 units
     float l = 0.f;
-    bool ok = true;
+    bool ok = true, again = false;               // again: this thread's row has to be computed once more
+    float rl = 0.f;
     for (int j = 0; j < ntx; ++j) {
       if (!(ok = pr_wait(&bars[L::kSFull + x], static_cast<uint32_t>(j) & 1, abort_flag, tmo))) break;
       tc_fence_after();
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       } else if (ok) {
         tc_fence_after();
         // No visible key: nothing was added, the row is zeros.
-        const float rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
+        rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
         bool finite = true;
         const uint32_t toa = split ? tmem + L::kColO + lane_base : to;
 #pragma unroll 1
@@ -786,10 +786,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
         }
         again = mine && !finite && fabsf(l) < __int_as_float(0x7F800000);
-        again_m = m == kNegInf ? 0.f : m;
-        again_rl = rl;
-        again_row = row;
-        again_visible = visible;
         if (mine && p.lse && (!split || x == 0))
           p.lse[head * p.lse_stride + sq.q0 + row] = visible > 0 ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
       }
@@ -800,7 +796,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       for (int d = 0; d < D; d += 8) z.store(dst + d);
       if (p.lse) p.lse[head * p.lse_stride + sq.q0 + row] = kNegInf;
     }
-    if constexpr (kCluster) {
+    if constexpr (!kCluster) {
+      // Split: the row's other thread has stored its half by then.
+      if (split) asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (again) prompt_row_again<E, D>(p, sq, row, head, visible, m == kNegInf ? 0.f : m, rl, 0, D);
+    } else {
       // Every warp of the cluster meets twice, after a wait that ran out too: the
       // CTAs' parts are written, and nobody leaves while they are read.
       __syncwarp();
@@ -819,8 +819,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (again) prompt_row_again<E, D>(p, sq, again_row, (warp >> 2) ? heads[1] : heads[0], again_visible, again_m, again_rl, 0,
-                                   D);
 }
 
 }  // namespace sage
