@@ -33,6 +33,10 @@
 // 1.0 times, for 2% of the time (64 sequences of 300 to 8192 keys 102.8 to 105.1
 // us; INT8 codes 107 to 112).  Sums, row maxima and the output stay in 32 bits.
 //
+// 64 sequences of 300 to 8192 keys x 8 KV heads (D = 128, E4M3, 583 MB) take 103 to
+// 105 us with the join, 5.5 to 5.7 TB/s; ALU 53% and issue 51% busy with turning
+// codes into f16.  One sequence of 3999 keys takes 8.3 us, two launches' latency.
+//
 // A CTA takes one chunk of keys of one segment (a sequence and a KV head with up
 // to 8 * NT of its query heads); its warps take 32-key tiles in turn and are
 // joined through shared memory; chunks are joined by token_join_kernel in a
