@@ -58,6 +58,12 @@
 // that is, is therefore computed once more from its visible keys alone, in 32
 // bits.  (A sum that is not finite comes from the row's own scores.)
 //
+// A visible score that is a NaN or +inf, or visible scores that are all -inf, leave
+// a row without a softmax: its output and its log-sum-exp are NaN.  The maximum of
+// a tile keeps a NaN, and where it is not below +inf the row's sum becomes a NaN and
+// stays one: the exponentials alone would not tell (the polynomial's clamp turns a
+// NaN into 2^-126).
+//
 // Bound by a row tile's chain (scores, softmax, weights, products) with two tiles
 // per SM: 8192 tokens x 32 heads, D = 128, take 536 to 545 us (1010 to 1025 TFLOP/s;
 // 585 us in a long run under the power cap), the tensor pipe 43% and the special-
@@ -210,6 +216,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// Maxima that are NaN where an argument is.
+__device__ __forceinline__ float pr_max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float pr_max(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // The weights of 64 keys, added up and written in 16-bit pairs to 32 TMEM
 // columns.  kMasked: scores of -inf weigh nothing, exactly (the polynomial never
 // gives less than 2^-126, so it takes no part there).
@@ -360,6 +378,7 @@ __device__ __forceinline__ void prompt_join(const PromptParams& p, const PromptS
       }
     }
     const int visible = p.causal ? min(sq.lk, max(0, row + off + 1)) : sq.lk;
+    if (visible > 0 && m == kNegInf) l = __int_as_float(0x7FFFFFFF);
     const float rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
     bool finite = true;
 #pragma unroll
@@ -663,10 +682,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         mx[c] = __uint_as_float(s[c][0]);
 #pragma unroll
         for (int i = 1; i < 31; i += 2)
-          mx[c] = fmax3(mx[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
-        mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
+          mx[c] = pr_max3(mx[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+        mx[c] = pr_max(mx[c], __uint_as_float(s[c][31]));
       }
-      const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+      const float tmax = pr_max(pr_max(mx[0], mx[1]), pr_max(mx[2], mx[3])) * sl;
+      if (!(tmax < __int_as_float(0x7F800000))) l = __int_as_float(0x7FFFFFFF);   // a NaN or +inf: no softmax
       if (L::kApart && j > 0) {      // P and O: the products of tile j - 1 are done
         if (!(ok = pr_wait(&bars[L::kPVDone + x], static_cast<uint32_t>(j - 1) & 1, abort_flag, tmo))) break;
         tc_fence_after();
@@ -755,7 +775,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
       } else if (ok) {
         tc_fence_after();
-        // No visible key: nothing was added, the row is zeros.
+        // No visible key: nothing was added, the row is zeros.  No score above -inf:
+        // no softmax.
+        if (visible > 0 && m == kNegInf) l = __int_as_float(0x7FFFFFFF);
         rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
         bool finite = true;
         const uint32_t toa = split ? tmem + L::kColO + lane_base : to;

@@ -429,7 +429,9 @@ SAGE_API sage_status sage_kv_read(sage_kv_cache cache, const int64_t* slots, int
  *      launch captured into a graph keeps them.
  * out: out [Tq, Hq, D] of the same type, apart from q, k and v; lse f32 [Hq, Tq], the natural log of
  *      the softmax denominator, or NULL.  A query that sees no key gets zeros
- *      and -inf.  Keys it does not see do not reach it, whatever they hold.
+ *      and -inf.  Keys it does not see do not reach it, whatever they hold.  A
+ *      query with a score that is a NaN or +inf, or with no score above -inf, has
+ *      no softmax: its out and lse are NaN.
  * Scores, sums and output accumulate in 32 bits; the weights are rounded to the
  * operands' type for the second product.
  */
