@@ -59,10 +59,8 @@
 // bits.  (A sum that is not finite comes from the row's own scores.)
 //
 // A visible score that is a NaN or +inf, or visible scores that are all -inf, leave
-// a row without a softmax: its output and its log-sum-exp are NaN.  The maximum of
-// a tile keeps a NaN, and where it is not below +inf the row's sum becomes a NaN and
-// stays one: the exponentials alone would not tell (the polynomial's clamp turns a
-// NaN into 2^-126).
+// a row without a softmax: its output and its log-sum-exp are NaN.  The weights
+// bring the first two into the row's sum (2^NaN, 2^(inf - inf)), which stays a NaN.
 //
 // Bound by a row tile's chain (scores, softmax, weights, products) with two tiles
 // per SM: 8192 tokens x 32 heads, D = 128, take 536 to 545 us (1010 to 1025 TFLOP/s;
@@ -178,35 +176,6 @@ __device__ __forceinline__ uint64_t make_sdesc_mn(uint32_t saddr, uint32_t piece
   return d;
 }
 
-// 2^x on the FMA and integer pipes, for the share of the weights that would
-// queue at the special-function unit (16 results a clock per SM): x = n + f with
-// n = round(x), 2^f by a polynomial with minimax relative error on [-1/2, 1/2]
-// (fitted by linear programming), n added to the exponent field.  Cubic (1.0e-4)
-// where the weights are rounded to bf16 (2^-9), quartic (2.8e-6) for fp16
-// (2^-12).  Two pairs of each 16: on 8192 tokens x 32 heads, D = 128 / 64, none
-// takes 549 / 406 us, two 536 / 400, four 559 / 411 (the FMA pipe, at 3 cycles a
-// packed operation, fills up); eight captions take 7.6 / 7.8 / 7.8.
-constexpr int kPrPolyOf16 = 2;
-__host__ __device__ constexpr bool pr_on_fma(int i) { return (i * kPrPolyOf16) % 16 < kPrPolyOf16; }
-template <bool kCubic>
-__device__ __forceinline__ f32x2_t pr_exp2_poly(f32x2_t x) {
-  x = x2_pack(__float_as_uint(fmaxf(x2_lo(x), kExp2Min)), __float_as_uint(fmaxf(x2_hi(x), kExp2Min)));
-  const f32x2_t round = x2_splat(kExp2Round);
-  const f32x2_t xr = x2_add(x, round);
-  const f32x2_t f = x2_sub(x, x2_sub(xr, round));
-  f32x2_t p;
-  if constexpr (kCubic) {
-    p = x2_fma(x2_splat(0.055009059607982635f), f, x2_splat(0.2422109693288803f));
-    p = x2_fma(p, f, x2_splat(0.6932829022407532f));
-  } else {
-    p = x2_fma(x2_splat(0.009582576341927052f), f, x2_splat(0.05590682849287987f));
-    p = x2_fma(p, f, x2_splat(0.24024106562137604f));
-    p = x2_fma(p, f, x2_splat(0.6931241154670715f));
-  }
-  p = x2_fma(p, f, x2_splat(1.f));
-  return x2_add_exponent(p, xr);
-}
-
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -216,25 +185,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-// Maxima that are NaN where an argument is.
-__device__ __forceinline__ float pr_max3(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float pr_max(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // The weights of 64 keys, added up and written in 16-bit pairs to 32 TMEM
-// columns.  kMasked: scores of -inf weigh nothing, exactly (the polynomial never
-// gives less than 2^-126, so it takes no part there).
-template <class E, bool kMasked>
+// columns.  All of them come from the special-function unit (2^-22 relative): a
+// share of two pairs in 16 on the FMA pipe (n + f, 2^f by a polynomial of about that
+// accuracy) took 549 to 557 us on 8192 tokens x 32 heads, D = 128, and 420 at D = 64,
+// against 541 to 549 and 392 to 405; with a cubic the 32-bit log-sum-exp was off by
+// 5e-5.
+template <class E>
 __device__ __forceinline__ void pr_weights(const uint32_t (&s0)[32], const uint32_t (&s1)[32], f32x2_t sl2,
                                            f32x2_t nref2, uint32_t col, f32x2_t (&sum)[4]) {
-  constexpr bool kBf16 = std::is_same<E, Bf16T>::value;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const uint32_t(&s)[32] = c == 0 ? s0 : s1;
@@ -242,13 +201,9 @@ __device__ __forceinline__ void pr_weights(const uint32_t (&s0)[32], const uint3
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const f32x2_t t = x2_fma(x2_pack(s[2 * i], s[2 * i + 1]), sl2, nref2);
-      f32x2_t w;
-      if (!kMasked && pr_on_fma(i))
-        w = pr_exp2_poly<kBf16>(t);
-      else
-        w = x2_pack(__float_as_uint(ex2_approx(x2_lo(t))), __float_as_uint(ex2_approx(x2_hi(t))));
-      sum[i & 3] = x2_add(sum[i & 3], w);
-      pk[i] = E::pack(x2_lo(w), x2_hi(w));
+      const float w0 = ex2_approx(x2_lo(t)), w1 = ex2_approx(x2_hi(t));
+      sum[i & 3] = x2_add(sum[i & 3], x2_pack(__float_as_uint(w0), __float_as_uint(w1)));
+      pk[i] = E::pack(w0, w1);
     }
     tmem_st16(col + 16 * c, pk);
   }
@@ -682,11 +637,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         mx[c] = __uint_as_float(s[c][0]);
 #pragma unroll
         for (int i = 1; i < 31; i += 2)
-          mx[c] = pr_max3(mx[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
-        mx[c] = pr_max(mx[c], __uint_as_float(s[c][31]));
+          mx[c] = fmax3(mx[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+        mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
       }
-      const float tmax = pr_max(pr_max(mx[0], mx[1]), pr_max(mx[2], mx[3])) * sl;
-      if (!(tmax < __int_as_float(0x7F800000))) l = __int_as_float(0x7FFFFFFF);   // a NaN or +inf: no softmax
+      const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
       if (L::kApart && j > 0) {      // P and O: the products of tile j - 1 are done
         if (!(ok = pr_wait(&bars[L::kPVDone + x], static_cast<uint32_t>(j - 1) & 1, abort_flag, tmo))) break;
         tc_fence_after();
@@ -712,10 +666,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       f32x2_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (masked)
-          pr_weights<E, true>(s[2 * half], s[2 * half + 1], sl2, nref2, tp + 32 * half, sum);
-        else
-          pr_weights<E, false>(s[2 * half], s[2 * half + 1], sl2, nref2, tp + 32 * half, sum);
+        pr_weights<E>(s[2 * half], s[2 * half + 1], sl2, nref2, tp + 32 * half, sum);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();

@@ -233,3 +233,25 @@ def test_graph_with_clusters_beside_an_eager_call(adt):
     torch.cuda.synchronize()
     adt.sage_check()
     assert torch.equal(out, want) and torch.equal(other, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("low", [-0.125, -0.25, -0.3125, -0.5, -0.75])
+def test_log_sum_exp_keeps_32_bits(adt, dtype, low):
+    """Scores without rounding (one channel, powers and short fractions): key 2 scores 0, keys 0 and 1 of every 16
+    `low`, the others -40.  Each weight is off by 2^-21 at most (its exponential, with the argument's rounding), the sum
+    of 256 of them by 256 2^-24, the logarithm and the result by 2^-22 of themselves each."""
+    L, D = 256, 64
+    q, k = torch.zeros(128, 1, D, device="cuda"), torch.full((L, 1), -40.0, device="cuda")
+    q[..., 0] = 1
+    at = torch.arange(L, device="cuda") % 16 < 2
+    k[at] = low
+    k[2] = 0
+    k = torch.nn.functional.pad(k[..., None], (0, D - 1))
+    lse = torch.empty(1, 128, device="cuda")
+    out = adt.sage_attn_prompt(q.to(dtype), k.to(dtype), torch.ones_like(k).to(dtype), [0, 128], [0, L], lse=lse,
+                               causal=False, sm_scale=1.0)
+    want = math.log(1 + 32 * math.exp(low) + 223 * math.exp(-40.0))
+    tol = 2.0 ** -21 + L * 2.0 ** -24 + 2 * 2.0 ** -22 * abs(want)
+    assert float((lse.double() - want).abs().max()) <= tol
+    assert bool((out == 1).all())
