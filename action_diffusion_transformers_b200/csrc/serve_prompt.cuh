@@ -45,11 +45,15 @@
 // S_X(j+1) is issued as soon as the softmax has read S_X(j), and P_X(j) is
 // written once PV_X(j-1) has completed.
 //
-// The reference m of a row moves only when a score passes it by 2^8 (P stays
-// below 2^8 in 16 bits and the sums in 32 bits), so O is rescaled rarely.  P is
-// rounded to the operands' 16-bit type (bf16 2^-9 relative, fp16 2^-12, each
-// weight on its own): the tensor core multiplies equal types.  The row sum adds
-// the weights before that rounding; sums, references and O stay in 32 bits.
+// The reference m of a row moves only when a score passes the last one it was set by
+// by 2^8, so O is rescaled rarely.  P is rounded to the operands' 16-bit type (half a
+// step: bf16 2^-8 relative, fp16 2^-11, each weight on its own): the tensor core
+// multiplies equal types.  In fp16 the reference lies 2^7 below the score that set it:
+// P stays below 2^15 (65504 is the type's end), and the type's fixed step under 2^-14
+// costs 2^-32 of such a weight at most, so a long tail of small weights is not lost
+// (65535 keys of e^-18 each, a thousandth together, came out as 0 without it).  The
+// row sum adds the weights before that rounding; sums, references and O stay in 32
+// bits.
 //
 // Values in masked places: a masked score is replaced, never added to, so K may
 // hold anything there.  A masked weight is 0, but 0 times an infinity or a NaN
@@ -80,7 +84,9 @@ constexpr int kPrWarpMma = 8, kPrWarpLoad = 10;
 constexpr int kPrMaxSeq = 256;          // sequences per launch
 constexpr int kPrMaxCluster = 8;         // CTAs that share an item at most
 constexpr int kPrMaxOrder = 512;        // pairs up to which the host sorts them
-constexpr float kPrRaise = 8.f;
+constexpr float kPrRaise = 8.f;          // log2: a row's reference moves for a score this far above the last
+template <class E>
+constexpr float kPrLift = std::is_same<E, Fp16T>::value ? 7.f : 0.f;   // log2: largest weight as the reference moves
 
 template <int D>
 struct PrSmem {
@@ -645,8 +651,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (!(ok = pr_wait(&bars[L::kPVDone + x], static_cast<uint32_t>(j - 1) & 1, abort_flag, tmo))) break;
         tc_fence_after();
       }
-      if (__any_sync(0xFFFFFFFFu, tmax > m + kPrRaise)) {
-        const float m1 = fmaxf(m, tmax);
+      if (__any_sync(0xFFFFFFFFu, tmax > m + (kPrLift<E> + kPrRaise))) {
+        const float m1 = fmaxf(m, tmax - kPrLift<E>);
         const float alpha = m == kNegInf ? 0.f : ex2_approx(m - m1);
         l *= alpha;
         m = m1;

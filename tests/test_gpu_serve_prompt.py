@@ -255,3 +255,19 @@ def test_log_sum_exp_keeps_32_bits(adt, dtype, low):
     tol = 2.0 ** -21 + L * 2.0 ** -24 + 2 * 2.0 ** -22 * abs(want)
     assert float((lse.double() - want).abs().max()) <= tol
     assert bool((out == 1).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lq", [1, 300])
+def test_many_small_weights(adt, dtype, lq):
+    """65535 keys of e^-18 of the largest weight each, a thousandth together, carry a channel of their own."""
+    L, D = 65536, 64
+    q = torch.zeros(lq, 2, D, device="cuda", dtype=dtype)
+    q[..., 0] = 1
+    k = torch.zeros(L, 1, D, device="cuda", dtype=dtype)
+    k[1:, :, 0] = -18
+    v = torch.zeros(L, 1, D, device="cuda", dtype=dtype)
+    v[0, :, 32:], v[1:, :, :32] = 1, 1
+    lse = torch.empty(2, lq, device="cuda")
+    out = adt.sage_attn_prompt(q, k, v, [0, lq], [0, L], lse=lse, causal=False, sm_scale=1.0)
+    _compare(out, lse, q, k, v, [0, lq], [0, L], False, scale=1.0)
