@@ -59,8 +59,9 @@
 // hold anything there.  A masked weight is 0, but 0 times an infinity or a NaN
 // in a masked V row (a later token, another sequence's row in the same tile)
 // would spread to the row's output; a row whose output is not finite, with a sum
-// that is, is therefore computed once more from its visible keys alone, in 32
-// bits.  (A sum that is not finite comes from the row's own scores.)
+// that is, is therefore looked at again (prompt_rows_again): a NaN or an infinity
+// among its visible values stays, what came from masked ones goes.  (A sum that is
+// not finite comes from the row's own scores.)
 //
 // A visible score that is a NaN or +inf, or visible scores that are all -inf, leave
 // a row without a softmax: its output and its log-sum-exp are NaN.  The weights
@@ -71,7 +72,10 @@
 // 585 us in a long run under the power cap), the tensor pipe 43% and the special-
 // function unit 38% busy; D = 64 400 us, the special-function unit 52%.
 //
-// Every wait is bounded (see mbar_wait_bounded), as in sage_attn.cuh.
+// Every wait on a load or a product is bounded (see mbar_wait_bounded), as in
+// sage_attn.cuh.  The barriers of the softmax warps, of the CTA and of a cluster have
+// no limit of their own: every warp reaches them, after a wait that ran out too, and
+// what lies between two of them ends by itself.
 #pragma once
 #include "serve_rows.cuh"
 #include "serve_token.cuh"
@@ -102,7 +106,8 @@ struct PrSmem {
   static constexpr int kQFull = 0, kSFull = 2, kPVDone = 4, kPFull = 6, kSRead = 10, kFull = 12,
                        kEmpty = kFull + kBarSlots, kDrain = kEmpty + kBarSlots, kNumBars = kDrain + 2;
   static constexpr int kMisc = kBar + kNumBars * 8;
-  static constexpr int kTotal = kMisc + 16;
+  static constexpr int kAgain = kMisc + 16;                   // rows to be looked at again, a bit each: 4 words per tile
+  static constexpr int kTotal = kAgain + 32;
   static constexpr int kAlloc = kTotal + 1024;
   // An item alone: each of the two tiles has a ring of its own, of kHalf slots
   // (D = 128: Q_B's place is one of them).  At the end of a tile's ring, once it
@@ -220,47 +225,6 @@ __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, volatile
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, tmo));
 }
 
-// One row once more from its visible keys, 8 channels at a time, in 32 bits:
-// only for rows whose first result was not finite though their sum was.
-template <class E, int D>
-__device__ __noinline__ void prompt_row_again(const PromptParams& p, const PromptSeq& sq, int row, int h, int visible,
-                                              float m, float rl, int d0, int d1) {
-  using S = typename E::S;
-  const S* q = static_cast<const S*>(p.q) + static_cast<int64_t>(sq.q0 + row) * p.q_stride + static_cast<int64_t>(h) * D;
-  const int64_t hk = static_cast<int64_t>(h / p.G) * D;
-  S* out = static_cast<S*>(p.out) + static_cast<int64_t>(sq.q0 + row) * p.out_stride + static_cast<int64_t>(h) * D;
-  for (int d = d0; d < d1; d += 8) {
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < visible; ++j) {
-      const S* k = static_cast<const S*>(p.k) + static_cast<int64_t>(sq.k0 + j) * p.k_stride + hk;
-      const S* v = static_cast<const S*>(p.v) + static_cast<int64_t>(sq.k0 + j) * p.v_stride + hk;
-      float s = 0.f;
-      for (int c = 0; c < D; c += 8) {
-        Piece<E, 8> a, b;
-        float x[8], y[8];
-        a.load(q + c);
-        b.load(k + c);
-        a.get(x);
-        b.get(y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
-      }
-      const float w = ex2_approx(fmaf(s, p.scale_log2, -m));
-      Piece<E, 8> a;
-      float x[8];
-      a.load(v + d);
-      a.get(x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = fmaf(w, x[i], o[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= rl;
-    Piece<E, 8> r;
-    r.put(o);
-    r.store(out + d);
-  }
-}
-
 // All threads of all CTAs of the cluster, each warp whole.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -293,6 +257,196 @@ __device__ __forceinline__ float* prompt_part(uint8_t* smem) {
   return reinterpret_cast<float*>(smem + PrSmem<D>::kRing2);
 }
 
+// Row r of tile x is to be looked at again.  What that takes goes where the tile's Q
+// was (its products are done), so that no register holds it until then.
+struct PromptMark {
+  float2 stat[kPrTile];        // reference and 1 / sum of the rows concerned
+  PromptSeq seq;
+  int row0, head, c0, c1;      // first row of the tile, channels
+};
+template <int D>
+__device__ __forceinline__ PromptMark* prompt_marks(uint8_t* smem, int x) {
+  return reinterpret_cast<PromptMark*>(smem + PrSmem<D>::kQ + x * PrSmem<D>::kTileBytes);
+}
+template <int D>
+__device__ __forceinline__ uint32_t* prompt_marked(uint8_t* smem) {
+  return reinterpret_cast<uint32_t*>(smem + PrSmem<D>::kAgain);
+}
+template <int D>
+__device__ __forceinline__ void prompt_mark(uint8_t* smem, int x, int r, float m, float rl, const PromptSeq& sq, int row0,
+                                            int head, int c0, int c1) {
+  PromptMark* mark = prompt_marks<D>(smem, x);
+  mark->stat[r] = make_float2(m, rl);
+  mark->seq = sq;
+  mark->row0 = row0;
+  mark->head = head;
+  mark->c0 = c0;
+  mark->c1 = c1;
+  atomicOr(prompt_marked<D>(smem) + 4 * x + r / 32, 1u << (r & 31));
+}
+
+// Rows whose stored output is not finite in some of the channels c0 .. c1 - 1 though
+// their sum is, by a whole warp: those of the bits of `todo`, in order (each sees no
+// fewer keys than the one before).  A NaN or an infinity in a visible row of V
+// decides its channel, whatever the weights (all above 0): V is added up, 2^-40 of
+// each value, until nothing can change any more, once for all rows of the warp.  Where
+// that sum is finite, what spoilt the channel was masked, and the weights are formed
+// again, four rows at a time, in 32 bits, a key per lane, and already divided by the
+// row's sum (so that finite values near the type's end add up).
+// The softmax warps' last act, behind the point where all warps have met: nobody waits
+// for them any more, and nothing is held in registers for it before (called where the
+// rows are stored, it made 8192 tokens x 32 heads 562 us instead of 535).  2048 tokens
+// x 8 heads, clean 38 us: one NaN token in front 76, an infinity in every seventh 120,
+// a NaN in the last token, whose row tile is formed again, 2700.
+template <class E, int D>
+__device__ __forceinline__ void prompt_rows_again(const PromptParams& p, const PromptMark& mark, uint32_t todo) {
+  using S = typename E::S;
+  constexpr int kBatch = 16, kRows = 4;
+  const int lane = threadIdx.x & 31, r0 = threadIdx.x & (kPrTile - 32);
+  const PromptSeq sq = mark.seq;
+  const int c0 = mark.c0, c1 = mark.c1, head = mark.head, row0 = mark.row0;
+  const int pieces = (c1 - c0) / 8, step = 32 / pieces;      // lanes of a row of V, rows that a warp reads at once
+  const int sub = lane / pieces, c = c0 + (lane - sub * pieces) * 8;
+  const int64_t hk = static_cast<int64_t>(head / p.G) * D, hq = static_cast<int64_t>(head) * D;
+  const S* v = static_cast<const S*>(p.v) + sq.k0 * p.v_stride + hk + c;
+  const S* k = static_cast<const S*>(p.k) + sq.k0 * p.k_stride + hk;
+  const S* q = static_cast<const S*>(p.q) + sq.q0 * p.q_stride + hq;
+  S* out = static_cast<S*>(p.out) + sq.q0 * p.out_stride + hq + c;
+  float seen[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // of the keys before `at` that this lane reads
+  int at = 0;
+  auto finite = [](float x) { return fabsf(x) < __int_as_float(0x7F800000); };
+  auto bits = [](const float(&x)[8], auto is) {              // a bit per channel
+    uint32_t b = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b |= static_cast<uint32_t>(is(x[e])) << e;
+    return b;
+  };
+  while (todo) {
+    // Up to kRows rows whose weights are wanted: the channels concerned, and the row's
+    // place, keys, reference and 1 / sum.
+    uint32_t want[kRows];
+    int r[kRows], vis[kRows], most = 0, n = 0;
+    float ref[kRows], part[kRows];
+#pragma unroll
+    for (int g = 0; g < kRows; ++g) want[g] = r[g] = vis[g] = 0, ref[g] = part[g] = 0.f;
+    while (todo && n < kRows) {
+      const int src = __ffs(todo) - 1;
+      const int ri = row0 + r0 + src, vi = p.causal ? min(sq.lk, max(0, ri + 1 + sq.lk - sq.lq)) : sq.lk;
+      todo &= todo - 1;
+      Piece<E, 8> got;
+      float x[8], all[8];
+      got.load(out + ri * p.out_stride);
+      got.get(x);
+      const uint32_t lost = bits(x, [&](float y) { return !finite(y); });
+      while (at < vi) {
+        uint32_t done = bits(seen, [](float y) { return y != y; });
+        for (int s = pieces; s < 32; s <<= 1) done |= __shfl_xor_sync(0xFFFFFFFFu, done, s);
+        if (!__any_sync(0xFFFFFFFFu, lost & ~done)) break;
+        Piece<E, 8> a[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int j = at + i * step + sub;
+          a[i] = Piece<E, 8>{};
+          if (j < vi) a[i].load(v + j * p.v_stride);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          float y[8];
+          a[i].get(y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) seen[e] = fmaf(y[e], 0x1p-40f, seen[e]);
+        }
+        at = min(vi, at + kBatch * step);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        all[e] = seen[e];
+        for (int s = pieces; s < 32; s <<= 1) all[e] += __shfl_xor_sync(0xFFFFFFFFu, all[e], s);
+      }
+      const uint32_t own = lost & bits(all, [&](float y) { return !finite(y); });
+      if (sub == 0 && own) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (own >> e & 1) x[e] = all[e];
+        got.put(x);
+        got.store(out + ri * p.out_stride);
+      }
+      if (__any_sync(0xFFFFFFFFu, lost & ~own)) {
+        const float2 st = mark.stat[r0 + src];
+        most = vi;
+#pragma unroll
+        for (int g = 0; g < kRows; ++g)
+          if (g == n) want[g] = lost & ~own, r[g] = ri, vis[g] = vi, ref[g] = st.x, part[g] = st.y;
+        ++n;
+      }
+    }
+    if (n == 0) break;
+    float o[kRows][8];
+#pragma unroll
+    for (int g = 0; g < kRows; ++g)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[g][e] = 0.f;
+    for (int j0 = 0; j0 < most; j0 += 32) {
+      float w[kRows];
+      const S* kj = k + min(j0 + lane, most - 1) * p.k_stride;
+#pragma unroll
+      for (int g = 0; g < kRows; ++g) w[g] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 8) {
+        Piece<E, 8> b;
+        float y[8];
+        b.load(kj + d);
+        b.get(y);
+#pragma unroll
+        for (int g = 0; g < kRows; ++g) {
+          Piece<E, 8> a;
+          float x[8];
+          a.load(q + r[g] * p.q_stride + d);
+          a.get(x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[g] = fmaf(x[e], y[e], w[g]);
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < kRows; ++g)
+        w[g] = j0 + lane < vis[g] ? ex2_approx(fmaf(w[g], p.scale_log2, -ref[g])) * part[g] : 0.f;
+#pragma unroll 4
+      for (int i = 0; i < pieces; ++i) {
+        const int j = i * step + sub;
+        Piece<E, 8> b;
+        float y[8];
+        b.load(v + min(j0 + j, most - 1) * p.v_stride);
+        b.get(y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = finite(y[e]) ? y[e] : 0.f;    // masked, or in a channel that is decided
+#pragma unroll
+        for (int g = 0; g < kRows; ++g) {
+          const float wj = __shfl_sync(0xFFFFFFFFu, w[g], j);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[g][e] = fmaf(wj, y[e], o[g][e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < kRows; ++g) {
+      for (int s = pieces; s < 32; s <<= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[g][e] += __shfl_xor_sync(0xFFFFFFFFu, o[g][e], s);
+      if (sub == 0 && want[g]) {
+        Piece<E, 8> got;
+        float x[8];
+        got.load(out + r[g] * p.out_stride);
+        got.get(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (want[g] >> e & 1) x[e] = o[g][e];
+        got.put(x);
+        got.store(out + r[g] * p.out_stride);
+      }
+    }
+  }
+}
+
 // O = sum_c 2^(m_c - m) O_c / sum_c 2^(m_c - m) l_c over the CTAs c of the cluster,
 // in their order; each CTA takes a share of the rows, a thread 8 channels.  For the
 // softmax warps: the others have given their registers away.
@@ -306,6 +460,7 @@ __device__ __forceinline__ void prompt_join(const PromptParams& p, const PromptS
   for (int i = threadIdx.x; i < share * kPieces; i += 32 * kPrWarpMma) {
     const int r = rank * share + i / kPieces, d = (i % kPieces) * 8, row = row0 + r;
     if (r >= kPrTile || row >= sq.lq) continue;
+    const int visible = p.causal ? min(sq.lk, max(0, row + off + 1)) : sq.lk;
     const uint32_t stat = smem_u32(prompt_stat<D>(smem) + r);
     const uint32_t part = smem_u32(prompt_part<D>(smem) + r * PrSmem<D>::kPartStride + d);
     float m = kNegInf, l = 0.f;
@@ -338,7 +493,6 @@ __device__ __forceinline__ void prompt_join(const PromptParams& p, const PromptS
         }
       }
     }
-    const int visible = p.causal ? min(sq.lk, max(0, row + off + 1)) : sq.lk;
     if (visible > 0 && m == kNegInf) l = __int_as_float(0x7FFFFFFF);
     const float rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
     bool finite = true;
@@ -347,14 +501,11 @@ __device__ __forceinline__ void prompt_join(const PromptParams& p, const PromptS
       finite = finite && fabsf(o[k]) < __int_as_float(0x7F800000);
       o[k] *= rl;
     }
-    if (finite || !(fabsf(l) < __int_as_float(0x7F800000))) {
-      Piece<E, 8> pc;
-      pc.put(o);
-      pc.store(static_cast<S*>(p.out) + static_cast<int64_t>(sq.q0 + row) * p.out_stride +
-               static_cast<int64_t>(head) * D + d);
-    } else {
-      prompt_row_again<E, D>(p, sq, row, head, visible, m == kNegInf ? 0.f : m, rl, d, d + 8);
-    }
+    Piece<E, 8> pc;
+    pc.put(o);
+    pc.store(static_cast<S*>(p.out) + static_cast<int64_t>(sq.q0 + row) * p.out_stride +
+             static_cast<int64_t>(head) * D + d);
+    if (!finite && fabsf(l) < __int_as_float(0x7F800000)) prompt_mark<D>(smem, 0, r, m, rl, sq, row0, head, 0, D);
     if (p.lse && d == 0)
       p.lse[head * p.lse_stride + sq.q0 + row] = visible > 0 ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
   }
@@ -456,6 +607,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // P, S read: one arrival per softmax warp; a ring slot is empty when all tiles that read it have
       mbar_init(&bars[i], i >= L::kPFull && i < L::kFull ? 4 : i >= L::kEmpty && i < L::kDrain && !split ? 2 : 1);
     *abort_flag = 0;
+    for (int i = 0; i < 8; ++i) prompt_marked<D>(smem)[i] = 0;
     fence_mbar_init();
   }
   if (tid == 32 * kPrWarpLoad) {
@@ -595,6 +747,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     cluster_sync();
     cluster_sync();
    }
+   __syncwarp();
+   tc_fence_before();
+   __syncthreads();
+   if (warp == kPrWarpMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+   }
   } else {
     // ------------------------------------------------------------ softmax
     regs_inc<kPrRegsSoftmax>();
@@ -612,8 +771,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const int visible = p.causal ? min(sq.lk, max(0, row + off + 1)) : sq.lk;
     float m = kNegInf;                             // reference, log2 units
     float l = 0.f;
-    bool ok = true, again = false;               // again: this thread's row has to be computed once more
-    float rl = 0.f;
+    bool ok = true;
     for (int j = 0; j < ntx; ++j) {
       if (!(ok = pr_wait(&bars[L::kSFull + x], static_cast<uint32_t>(j) & 1, abort_flag, tmo))) break;
       tc_fence_after();
@@ -735,7 +893,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // No visible key: nothing was added, the row is zeros.  No score above -inf:
         // no softmax.
         if (visible > 0 && m == kNegInf) l = __int_as_float(0x7FFFFFFF);
-        rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
+        const float rl = visible > 0 ? __fdiv_rn(1.f, l) : 0.f;
         bool finite = true;
         const uint32_t toa = split ? tmem + L::kColO + lane_base : to;
 #pragma unroll 1
@@ -769,9 +927,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
           }
         }
-        again = mine && !finite && fabsf(l) < __int_as_float(0x7F800000);
         if (mine && p.lse && (!split || x == 0))
           p.lse[head * p.lse_stride + sq.q0 + row] = visible > 0 ? (m + log2f(l)) * 0.69314718055994531f : kNegInf;
+        if (mine && !finite && fabsf(l) < __int_as_float(0x7F800000)) prompt_mark<D>(smem, x, r, m, rl, sq, row - r, head, cb0, cb1);
       }
     } else if (mine) {
       Piece<E, 8> z;
@@ -780,11 +938,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       for (int d = 0; d < D; d += 8) z.store(dst + d);
       if (p.lse) p.lse[head * p.lse_stride + sq.q0 + row] = kNegInf;
     }
-    if constexpr (!kCluster) {
-      // Split: the row's other thread has stored its half by then.
-      if (split) asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (again) prompt_row_again<E, D>(p, sq, row, head, visible, m == kNegInf ? 0.f : m, rl, 0, D);
-    } else {
+    if constexpr (kCluster) {
       // Every warp of the cluster meets twice, after a wait that ran out too: the
       // CTAs' parts are written, and nobody leaves while they are read.
       __syncwarp();
@@ -793,15 +947,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       __syncwarp();
       cluster_sync();
     }
-  }
-
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  if (*abort_flag && tid == 0) atomicExch(p.err, 1);
-  if (warp == kPrWarpMma) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && tid == 0) atomicExch(p.err, 1);
+    const uint32_t todo = prompt_marked<D>(smem)[warp];
+    if (todo) prompt_rows_again<E, D>(p, *prompt_marks<D>(smem, x), todo);
   }
 }
 
