@@ -25,8 +25,10 @@
 // per head so that its largest channel lies in [1, 2) and rounded to f16:
 // channels above 2^-14 of the largest keep every bit, the others are off by at
 // most 2^-25 of it.  P carries the V scale of its key and a power of two per
-// head that keeps the largest weight met so far near 1, so its rounding to f16
-// (2^-11 relative) is never an underflow of weights that matter.  That rounding is
+// head, set by the first weight above 0, that keeps the largest one met so far
+// near 1.  Its rounding to f16 is 2^-11 relative, and for weights below 2^-14 of the
+// largest 2^-25 of that one: 2^-16 of it over the up to 512 keys that a warp adds
+// (16 tiles of a chunk; each warp has a power of its own).  That rounding is
 // far below a bf16 output's own (2^-8), but equal to an fp16 output's: there P goes
 // in as two f16 parts (kFine), what the first leaves out being the second, which
 // takes the error against 64 bits from 1.4 times that of the output's rounding to
@@ -53,6 +55,10 @@ constexpr int kTokStages = 2;             // tiles in a warp's queue
 constexpr int kTokPerSm = 3;              // resident CTAs: the queues take 68 KB each at D = 128
 constexpr float kTokRaise = 8.f;          // the row max moves only when a score passes it by this (log2)
 constexpr float kTokMaxW = 2048.f;        // largest P before its power of two is renewed
+// Exponents of that power of two: the largest stands for "no weight above 0 yet", and
+// the first such weight passes kTokMaxW by it (or lies below 2^-107, where the V scales
+// that the cache write gives end).
+constexpr int kTokMaxCf = 118, kTokMinCf = -126;
 
 struct TokenParams {
   const void* q;           // [B, Hq, D], q_stride elements per sequence
@@ -199,7 +205,7 @@ struct TokState {
   float m[NT][2];            // reference of the exponent, log2 (-inf: nothing seen)
   float l[NT][2];            // sum of 2^(x - m) over this lane's keys
   float w[NT][2];            // largest weight p * vs met, as of the last renewal
-  float cf[NT][2];           // power of two on the weights
+  float cf[NT][2];           // power of two on the weights (2^kTokMaxCf: none above 0 yet)
   float o[NT][D / 16][4];
 };
 
@@ -300,11 +306,11 @@ __device__ __forceinline__ void tok_step(const uint8_t* stage, int n, int have, 
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) wm = fmaxf(wm, __shfl_xor_sync(0xFFFFFFFFu, wm, o));
         wm = fmaxf(wm, st.w[b][c] * alpha);
-        // exponent of wm in [-100, 100]; wm = 0 keeps the factor
-        const int ex = min(max(static_cast<int>(__float_as_uint(wm) >> 23) - 127, -100), 100);
-        const float cf = wm > 0.f ? __uint_as_float(static_cast<uint32_t>(127 - ex) << 23) : st.cf[b][c];
-        // cf is a power of two, so dividing by it is exact
-        const float f = alpha * (cf * (1.f / st.cf[b][c]));
+        const int ex = min(max(127 - static_cast<int>(__float_as_uint(wm) >> 23), kTokMinCf), kTokMaxCf);
+        const float cf = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        // cf is a power of two, so dividing by it is exact; the quotient is below
+        // 2 / alpha, as wm is at least w * alpha
+        const float f = alpha == 0.f ? 0.f : alpha * (cf * (1.f / st.cf[b][c]));
         st.m[b][c] = m1;
         st.w[b][c] = wm;
         st.cf[b][c] = cf;
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
         st.m[blk][k] = kNegInf;
         st.l[blk][k] = 0.f;
         st.w[blk][k] = 0.f;
-        st.cf[blk][k] = 1.f;
+        st.cf[blk][k] = __uint_as_float(static_cast<uint32_t>(127 + kTokMaxCf) << 23);
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)

@@ -201,3 +201,28 @@ def test_no_sequences(adt):
     out = cache.attend(q, torch.empty(0, 3, dtype=torch.int32, device="cuda"),
                        torch.empty(0, dtype=torch.int32, device="cuda"), q.clone(), None)
     assert out.shape == (0, 4, 64) and math.prod(out.shape) == 0
+
+
+def _one_long(adt, L, fmt, dtype, D=128, seed=0):
+    """One sequence of L keys among 56 with 8 KV heads: its keys are one chunk, so each warp takes many tiles."""
+    return _setup(adt, [L] + [1] * 55, 16, 8, D, 32, fmt, dtype, seed=seed)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("int8", torch.bfloat16), ("e4m3", torch.float16), ("e4m3", torch.bfloat16),
+                                       ("int8", torch.float16)])
+@pytest.mark.parametrize("amax", [1.0, 1e-2, 1e-4])
+def test_v_rows_of_zeros_first(adt, fmt, dtype, amax):
+    """The power of two on the weights waits for the first weight that is not zero."""
+    L = 1500
+    cache, q, table, ln, slots = _one_long(adt, L, fmt, dtype, seed=17)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k = 0.2 * torch.randn(L, 8, 128, generator=g, device="cuda")
+    k[:200] *= 4                                                  # the reference does not rise any more
+    v = torch.randn(L, 8, 128, generator=g, device="cuda")
+    v = amax * v / v.abs().amax(-1, keepdim=True)
+    v[:200] = 0
+    cache.write(k.to(dtype), v.to(dtype), slots[:L])
+    out, lse = torch.empty_like(q.contiguous()), torch.empty(56, 16, device="cuda")
+    cache.attend(q, table, ln, out, _workspace(adt, q, cache, table), lse=lse)
+    adt.sage_check()
+    _compare(out[:1], lse[:1], cache, q[:1], [L], slots[:L])
