@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
   pdl_enter();
   using S = typename E::S;
   using Q = TokQueue<D>;
-  __shared__ float s_m[kTokWarps][8 * NT], s_l[kTokWarps][8 * NT];
+  __shared__ float s_m[kTokWarps][8 * NT], s_l[kTokWarps][8 * NT], s_u[kTokWarps][8 * NT];
   // The warps' queues; after the last tile the same bytes join the warps' O.
   extern __shared__ __align__(16) uint8_t tok_smem[];
   float(*s_o)[8 * NT][D + 4] = reinterpret_cast<float(*)[8 * NT][D + 4]>(tok_smem);
@@ -513,12 +513,12 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
         if (g == 0) {
           s_m[warp][h] = st.m[blk][k];
           s_l[warp][h] = l;
+          s_u[warp][h] = 1.f / st.cf[blk][k];           // exact: a power of two
         }
-        const float up = 1.f / st.cf[blk][k];           // exact: a power of two
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
           *reinterpret_cast<float2*>(&s_o[warp][h][g * (D / 8) + 2 * i]) =
-              make_float2(st.o[blk][i][k] * up, st.o[blk][i][k + 2] * up);
+              make_float2(st.o[blk][i][k], st.o[blk][i][k + 2]);
       }
     }
     __syncthreads();
@@ -529,27 +529,32 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
 #pragma unroll
       for (int w = 1; w < kTokWarps; ++w) m = fmaxf(m, s_m[w][h]);
       const float ref = m == kNegInf ? 0.f : m;
-      float l = 0.f;
+      float l = 0.f, f[kTokWarps];
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kTokWarps; ++w) {
-        const float f = ex2_approx(s_m[w][h] - ref);
-        const float4 v = *reinterpret_cast<const float4*>(&s_o[w][h][d]);
-        l += f * s_l[w][h];
-        o.x += f * v.x;
-        o.y += f * v.y;
-        o.z += f * v.z;
-        o.w += f * v.w;
+        f[w] = ex2_approx(s_m[w][h] - ref);
+        l += f[w] * s_l[w][h];
       }
       const float r = l == 0.f ? 0.f : __fdiv_rn(1.f, l);
       const float lse2 = l == 0.f ? kNegInf : m + log2f(l);
-      o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+      // Divided by the sum before the weights' power of two goes: values near the end
+      // of bf16 would pass that of binary32 otherwise.
+#pragma unroll
+      for (int w = 0; w < kTokWarps; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(&s_o[w][h][d]);
+        const float fr = f[w] * r, up = s_u[w][h];
+        o.x += fr * v.x * up;
+        o.y += fr * v.y * up;
+        o.z += fr * v.z * up;
+        o.w += fr * v.w * up;
+      }
       const int head = hk * p.G + h0 + h;
       const int64_t at = static_cast<int64_t>(b) * p.Hq + head;
       if (p.chunks == 1) {
         Piece<E, 4> v;
-        const float f[4] = {o.x, o.y, o.z, o.w};
-        v.put(f);
+        const float out[4] = {o.x, o.y, o.z, o.w};
+        v.put(out);
         v.store(static_cast<S*>(p.out) + b * p.out_stride + static_cast<int64_t>(head) * D + d);
         if (d == 0 && p.lse) p.lse[at] = lse2 * 0.69314718055994531f;
       } else {
@@ -561,8 +566,9 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
 }
 
 // Joins the chunks of one (sequence, query head), and writes the rows of empty
-// sequences: kWarps warps per row, weights 2^(lse - max), each warp its chunks in
-// order, then the warps in order.
+// sequences: kWarps warps per row, weights 2^(lse - max - 20), each warp its chunks in
+// order, then the warps in order.  (2^-20: the sum over the chunks, at most 2^19, of
+// values near the end of bf16 stays within binary32.)
 constexpr int kJoinThreads = 128;
 template <class E, int D, int kWarps>
 __global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const __grid_constant__ TokenParams p) {
@@ -582,6 +588,7 @@ __global__ void __launch_bounds__(kJoinThreads) token_join_kernel(const __grid_c
   for (int i = lane; i < parts; i += 32) m = fmaxf(m, lse[i]);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  m += 20.f;
   const float ref = m == kNegInf ? 0.f : m;
   float l = 0.f, o[V];
 #pragma unroll

@@ -226,3 +226,35 @@ def test_v_rows_of_zeros_first(adt, fmt, dtype, amax):
     cache.attend(q, table, ln, out, _workspace(adt, q, cache, table), lse=lse)
     adt.sage_check()
     _compare(out[:1], lse[:1], cache, q[:1], [L], slots[:L])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_v_of_every_size(adt, fmt):
+    """V near both ends of bfloat16's range, and both in one sequence.  A weight below 2^-126 of the largest is 0 in 32
+    bits, so the earlier values may be missing from the third case: up to L 2^-126 3e38 < 2^13 = 8192."""
+    L = 1500
+    cache, q, table, ln, slots = _one_long(adt, L, fmt, torch.bfloat16, seed=18)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ws = _workspace(adt, q, cache, table)
+    out, lse = torch.empty_like(q.contiguous()), torch.empty(56, 16, device="cuda")
+    n = torch.randn(L, 8, 128, generator=g, device="cuda")
+    n = n / n.abs().amax(-1, keepdim=True)
+    plain = 0.2 * torch.randn(L, 8, 128, generator=g, device="cuda")
+    late = plain.clone()
+    late[700:] += 8 * q[0].float().view(8, 2, 128).mean(1)       # scores far above the earlier ones
+    for k, first, then in ((plain, 3e38, 3e38), (plain, 1e-27, 1e-27), (late, 3e38, 1e-27), (late, 1e-27, 3e38),
+                           (plain, 1e-27, 3e38)):
+        v = n * first
+        v[700:] = n[700:] * then
+        cache.write(k.bfloat16(), v.bfloat16(), slots[:L])
+        cache.attend(q, table, ln, out, ws, lse=lse)
+        if first > then and k is late:
+            x, y = cache.k_codes.double() * cache.k_scale.double()[..., None], cache.v_codes.double() * cache.v_scale.double()[..., None]
+            x, y = (z.permute(0, 2, 1, 3).reshape(-1, 8, 128)[slots[:L]] for z in (x, y))
+            for h in range(16):
+                ref, _, tol, _ = attend(q[0, h][None].double(), x[:, h // 2], y[:, h // 2],
+                                        torch.tensor([L], device="cuda"), 128 ** -0.5, 2.0 ** -11)
+                err = (out[0, h][None].double() - ref).abs()
+                assert bool((err <= 2.0 ** -8 * (ref.abs() + tol) + tol + 8192).all()), h
+        else:
+            _compare(out[:1], lse[:1], cache, q[:1], [L], slots[:L])
