@@ -456,7 +456,10 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
       if (ex == 128 || bits == 0) ex = 0;
       ex = max(ex, -126);
       const float dn = __uint_as_float(static_cast<uint32_t>(127 - min(ex, 126)) << 23);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+      // An infinity or a NaN in q: every score is one of the two, so the head has no
+      // softmax (all scores -inf would pass for a sequence without keys).
+      const float up = bits < 0x7F800000u ? __uint_as_float(static_cast<uint32_t>(127 + ex) << 23)
+                                          : __uint_as_float(0x7FFFFFFFu);
       const float rest = ex == 127 ? 0.5f : 1.f;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {

@@ -461,7 +461,9 @@ SAGE_API sage_status sage_attn_prompt(const void* q, const void* k, const void* 
  *      sets the launch and the workspace.  sm_scale <= 0 selects 1/sqrt(D).
  * out: out [B, Hq, D] of q's type; lse f32 [B, Hq] or NULL; zeros and -inf for a
  *      sequence without keys.  A page outside the cache is left out and
- *      recorded.
+ *      recorded.  A head of q that holds a NaN or an infinity, and one that sees a
+ *      key whose K scale is a NaN, has no softmax: its out and lse are NaN.  A V
+ *      scale that is a NaN reaches out alone.
  * workspace: sage_attn_token_workspace_bytes() bytes, 256-byte aligned; calls
  * on one stream may share it, graphs that run at the same time may not.
  */

@@ -258,3 +258,23 @@ def test_v_of_every_size(adt, fmt):
                 assert bool((err <= 2.0 ** -8 * (ref.abs() + tol) + tol + 8192).all()), h
         else:
             _compare(out[:1], lse[:1], cache, q[:1], [L], slots[:L])
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_query_that_is_no_number(adt, bad):
+    """Every score of such a head is an infinity or no number, so it has no softmax; its neighbours are as before."""
+    lens, Hq, Hk, D, ps = [70, 300, 0], 4, 2, 64, 16
+    for fmt, dtype in (("int8", torch.bfloat16), ("e4m3", torch.float16)):
+        cache, q, table, ln, slots = _setup(adt, lens, Hq, Hk, D, ps, fmt, dtype, seed=19, garbage=False)
+        k = torch.randn(370, Hk, D, device="cuda").abs() + 0.25
+        cache.write(-k.to(dtype), k.to(dtype), slots)            # one sign: no score is 0 times an infinity
+        ws = _workspace(adt, q, cache, table)
+        clean = cache.attend(q, table, ln, torch.empty_like(q.contiguous()), ws)
+        q = q.clone()
+        q[0, 1, 7] = q[1, 2, 7] = q[2, 0, 7] = bad
+        lse = torch.empty(3, Hq, device="cuda")
+        out = cache.attend(q, table, ln, torch.empty_like(clean), ws, lse=lse)
+        for b, h in ((0, 1), (1, 2)):
+            assert bool(torch.isnan(out[b, h]).all()) and bool(torch.isnan(lse[b, h]))
+            out[b, h] = clean[b, h]
+        assert torch.equal(out, clean) and bool((out[2] == 0).all())      # without keys: zeros
