@@ -113,7 +113,7 @@ int64_t token_tiles(int max_len) { return (static_cast<int64_t>(max_len) + sage:
 // with 444 chunks wanted and 13.4 with 1776, three of 2000 to 8000 keys 13.9 and
 // 20.5; 64 of 300 to 8192 keys 110 us with 4 tiles per warp, 103 with 8, 102 with
 // 16.)
-constexpr int kTokWant = 444, kTokPerMax = 16;
+constexpr int kTokWant = 148 * sage::kTokPerSm, kTokPerMax = 16;
 int token_per(int B, int Hk, int G, int max_len) {
   const int64_t tiles = token_tiles(max_len), w = sage::kTokWarps;
   const int64_t chunks = std::max<int64_t>(1, kTokWant / std::max<int64_t>(1, B * token_segs(Hk, G)));
@@ -124,13 +124,33 @@ int token_chunks(int max_len, int per) {
   return static_cast<int>(std::max<int64_t>(1, (token_tiles(max_len) + per - 1) / per));
 }
 
+// Most chunks of all sequences together in any call of up to B sequences and max_len
+// keys (0: the chunks' results need no workspace).  Fewer sequences are cut into more
+// chunks, and a shorter max_len into as many shorter ones, so this and not the call's
+// own number is what a workspace kept for many calls has to hold.  A call of b
+// sequences has at most as many chunks each as are wanted or as there are tiles for the
+// warps of one, and, where they are as long as may be, one per kTokPerMax tiles a warp;
+// from kTokWant sequences on only the latter counts, and grows with b.
+int64_t token_chunks_bound(int B, int Hk, int G, int max_len) {
+  const int64_t tiles = token_tiles(max_len), w = sage::kTokWarps, segs = token_segs(Hk, G);
+  int64_t most = 0;
+  auto take = [&](int64_t b) {
+    const int64_t wanted = std::max<int64_t>(1, kTokWant / (b * segs));
+    const int64_t chunks = std::max(std::min(wanted, (tiles + w - 1) / w), (tiles + kTokPerMax * w - 1) / (kTokPerMax * w));
+    if (chunks > 1) most = std::max(most, b * chunks);
+  };
+  for (int64_t b = 1; b <= std::min<int64_t>(B, kTokWant); ++b) take(b);
+  take(B);
+  return most;
+}
+
 // Workspace of the single-token attention: the chunks' results.
 struct TokenWs {
   size_t part_lse, total;
 };
-TokenWs token_ws(int B, int Hq, int D, int chunks) {
-  if (chunks <= 1) return {0, 0};
-  const size_t rows = static_cast<size_t>(B) * Hq * chunks;
+TokenWs token_ws(int64_t chunks, int Hq, int D) {              // chunks of all sequences
+  if (chunks == 0) return {0, 0};
+  const size_t rows = static_cast<size_t>(chunks) * Hq;
   const size_t o = (rows * D * 4 + 255) / 256 * 256;
   return {o, o + (rows * 4 + 255) / 256 * 256};
 }
@@ -659,7 +679,7 @@ sage_status sage_attn_prompt(const void* q, const void* k, const void* v, const 
 
 size_t sage_attn_token_workspace_bytes(int B, int Hq, int Hk, int D, int max_len) {
   if (B < 0 || max_len < 0 || (D != 64 && D != 128) || check_heads(Hq, Hk) != SAGE_OK) return 0;
-  return B == 0 ? 0 : token_ws(B, Hq, D, token_chunks(max_len, token_per(B, Hk, Hq / Hk, max_len))).total;
+  return B == 0 ? 0 : token_ws(token_chunks_bound(B, Hk, Hq / Hk, max_len), Hq, D).total;
 }
 
 sage_status sage_attn_token(const void* q, const sage_token* a, sage_kv_cache cache, void* out, float* lse,
@@ -691,7 +711,7 @@ sage_status sage_attn_token(const void* q, const sage_token* a, sage_kv_cache ca
   const int G = a->Hq / cache.Hk;
   p.per = token_per(a->B, cache.Hk, G, a->max_len);
   p.chunks = token_chunks(a->max_len, p.per);
-  const TokenWs ws = token_ws(a->B, a->Hq, cache.D, p.chunks);
+  const TokenWs ws = token_ws(p.chunks > 1 ? static_cast<int64_t>(a->B) * p.chunks : 0, a->Hq, cache.D);
   if (ws.total > 0) {
     if (!workspace) return fail(SAGE_ERR_WORKSPACE, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)

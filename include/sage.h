@@ -465,7 +465,9 @@ SAGE_API sage_status sage_attn_prompt(const void* q, const void* k, const void* 
  *      key whose K scale is a NaN, has no softmax: its out and lse are NaN.  A V
  *      scale that is a NaN reaches out alone.
  * workspace: sage_attn_token_workspace_bytes() bytes, 256-byte aligned; calls
- * on one stream may share it, graphs that run at the same time may not.
+ * on one stream may share it, graphs that run at the same time may not.  Bytes
+ * enough for B sequences and max_len keys are enough for fewer and for shorter
+ * ones too (of the same heads and D), so one buffer serves a batch that thins out.
  */
 typedef struct {
   int B, Hq;

@@ -305,3 +305,26 @@ def test_python_layer_refuses_layouts(adt):
         token(ws=torch.zeros(64)[::2])
     with pytest.raises(ValueError, match="q must be|out must be"):
         token(q=narrow)
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(32, 8, 128), (4, 4, 64), (40, 1, 64), (512, 8, 128), (1, 1, 128)])
+def test_a_workspace_serves_fewer_and_shorter_sequences(adt, Hq, Hk, D):
+    """A batch that thins out, or a tighter max_len, needs no more than the largest one asked for; the call itself takes
+    what its own chunks need (checked on the host, in front of the launch)."""
+    need = lambda B, L: adt.attn_token_workspace_bytes(B, Hq, Hk, D, L)  # noqa: E731
+    lens = [0, 1, 32, 128, 129, 384, 512, 1000, 2047, 2048, 2049, 8192, 100000]
+    batches = [1, 2, 3, 8, 16, 27, 32, 55, 56, 64, 111, 222, 443, 444, 445, 1000]
+    for i, B in enumerate(batches):
+        for j, L in enumerate(lens):
+            assert need(B, L) >= max([need(b, L) for b in batches[:i]] + [need(B, x) for x in lens[:j]] + [0]), (B, L)
+    if _gpu():
+        return                                                   # valid calls on made-up addresses: only without a GPU
+    c = _cache(adt, Hk=Hk, D=D, num_pages=1 << 20, page_size=64)
+    for B, L in ((64, 2048), (27, 8192), (444, 100000), (1000, 512)):
+        ws = need(B, L)
+        for b in batches:
+            for x in lens:
+                if b <= B and x <= L:
+                    p = adt.SageToken(b, Hq, 0, 0, 0, FAKE, 4096, FAKE, x, 0.0)
+                    st = adt._lib.sage_attn_token(FAKE, ctypes.byref(p), c, FAKE, None, FAKE << 8 if ws else None, ws, None)
+                    assert st == 4, (B, L, b, x)
