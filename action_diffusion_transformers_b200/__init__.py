@@ -363,9 +363,17 @@ def sage_kv_read(slots, k_codes, k_scale, v_codes, v_scale, k, v, stream=None):
 def sage_attn_prompt(q, k, v, cu_q, cu_k=None, out=None, lse=None, causal=True, sm_scale=0.0, stream=None):
     """Attention over packed sequences: q [Tq, Hq, D], k, v [Tk, Hk, D] BF16 or FP16; cu_q, cu_k host offsets, a list or a
     CPU tensor (cu_k None: cu_q).  causal: query i of a sequence sees keys j <= i + Lk - Lq.  lse: float32 [Hq, Tq] or
-    None.  Returns out."""
+    None.  Returns out; without one given it is allocated on the stream of the call."""
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if stream is None or not q.is_cuda:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            # the memory belongs to the stream that writes it: allocated for the current one, it could be in use there
+            # still, or again, while the given one writes
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=q.device)
+            with torch.cuda.stream(stream):
+                out = torch.empty_like(q, memory_format=torch.contiguous_format)
     status = _serve_ext.attn_prompt(q, k, v, cu_q, cu_k, out, lse, causal, sm_scale, stream)
     if status:
         raise SageError(status, "sage_attn_prompt")

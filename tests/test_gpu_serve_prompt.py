@@ -271,3 +271,26 @@ def test_many_small_weights(adt, dtype, lq):
     lse = torch.empty(2, lq, device="cuda")
     out = adt.sage_attn_prompt(q, k, v, [0, lq], [0, L], lse=lse, causal=False, sm_scale=1.0)
     _compare(out, lse, q, k, v, [0, lq], [0, L], False, scale=1.0)
+
+
+def test_own_output_on_a_given_stream(adt):
+    """An output that the call makes belongs to the stream that writes it: released at once, its memory is not handed
+    to the current stream while that one still writes."""
+    q, k, v = _inputs([300], [300], 2, 1, 64, torch.bfloat16, seed=40)
+    want = adt.sage_attn_prompt(q, k, v, [0, 300])
+    torch.cuda.synchronize()
+    for side in (torch.cuda.Stream(),):
+        for given in (side, side.cuda_stream):
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(20_000_000)
+            out = adt.sage_attn_prompt(q, k, v, [0, 300], stream=given)
+            at = out.data_ptr()
+            keep = [torch.zeros_like(want) for _ in range(4)]
+            del out
+            keep += [torch.zeros_like(want) for _ in range(4)]
+            side.synchronize()
+            assert at not in [t.data_ptr() for t in keep] and all(not bool(t.any()) for t in keep)
+            out = adt.sage_attn_prompt(q, k, v, [0, 300], stream=given)
+            side.synchronize()
+            assert torch.equal(out, want)
