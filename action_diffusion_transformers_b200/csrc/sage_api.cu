@@ -823,11 +823,13 @@ sage_status sage_check(sage_stream_t stream) {
   int flag[2] = {0, 0};
   e = cudaMemcpy(flag, err, sizeof(flag), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "reading the device error words");
-  if (flag[0] || flag[1]) {
-    const int zero[2] = {0, 0};
-    e = cudaMemcpy(err, zero, sizeof(zero), cudaMemcpyHostToDevice);
-    if (e != cudaSuccess) return cuda_fail(e, "clearing the device error words");
-    if (flag[0])
+  for (int i = 0; i < 2; ++i) {
+    if (!flag[i]) continue;
+    // One is reported and cleared; the other stays for the next call.
+    const int zero = 0;
+    e = cudaMemcpy(err + i, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    if (e != cudaSuccess) return cuda_fail(e, "clearing the device error word");
+    if (i == 0)
       return fail(SAGE_ERR_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (timeout %lld ns)",
                   (long long)g_timeout_ns.load());
     return fail(SAGE_ERR_INVALID_ARG, "a kernel met a slot or page index outside the cache and skipped it");

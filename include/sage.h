@@ -487,7 +487,8 @@ SAGE_API sage_status sage_attn_token(const void* q, const sage_token* p, sage_kv
 /* Synchronises `stream`, then reports and clears a device-side wait timeout
  * raised by any kernel of this library (SAGE_ERR_DEVICE_TIMEOUT), a slot or page
  * index outside a KV cache (SAGE_ERR_INVALID_ARG), or a CUDA error
- * (SAGE_ERR_CUDA); SAGE_OK otherwise. */
+ * (SAGE_ERR_CUDA); SAGE_OK otherwise.  Of the first two one is reported and cleared
+ * per call, the timeout first.  Both are the current device's. */
 SAGE_API sage_status sage_check(sage_stream_t stream);
 
 /* Bound, in nanoseconds, on every wait inside the library's kernels (default

@@ -265,3 +265,11 @@ def test_no_tokens(adt):
     cache.read(none, e, e)
     adt.sage_rope(e, e, none, adt.RopePlan(64))
     adt.sage_check()
+
+
+def test_a_bad_slot_and_a_wait_that_ran_out_are_both_reported(adt):
+    cache = adt.KVCache(2, 16, 2, 64)
+    x = torch.ones(1, 2, 64, device="cuda", dtype=torch.bfloat16)
+    cache.write(x, x, torch.tensor([32], device="cuda"))
+    adt.selftest_wait_timeout(1_000_000)
+    assert [adt.sage_check_status() for _ in range(3)] == [5, 1, 0]
