@@ -15,9 +15,9 @@ and so do the serving calls beside them:
 
 This module only marshals arguments: torch tensors provide device memory and
 the current CUDA stream; every step of the computation runs in the library's
-CUDA kernels.  Importing it loads libsage.so, and the extension module that
-hands tensors to the serving calls, and raises ImportError if they have not been
-built (there is no fallback implementation).
+CUDA kernels.  Importing it loads libsage.so and raises ImportError if that has
+not been built; a serving call raises it if the extension module that hands
+tensors to them does not load (there is no fallback implementation).
 """
 from __future__ import annotations
 
@@ -33,7 +33,21 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libsage.so is not built ({LIB_PATH}); run "
                       "`python -m action_diffusion_transformers_b200.build`")
 _lib = ctypes.CDLL(LIB_PATH)
-from . import _serve_ext  # noqa: E402  (built beside the library)
+try:
+    from . import _serve_ext  # built beside the library, for the installed torch and Python
+except ImportError as _e:
+
+    class _NoServeExt:
+        """The quantized attention needs libsage.so alone; the serving calls raise."""
+
+        def __init__(self, why):
+            self.why = why
+
+        def __getattr__(self, name):
+            raise ImportError("the serving calls' extension module _serve_ext.so does not load with this torch and "
+                              f"Python ({self.why}); run `python -m action_diffusion_transformers_b200.build`")
+
+    _serve_ext = _NoServeExt(str(_e))
 
 SAGE_OK = 0
 STATUS_NAMES = {0: "SAGE_OK", 1: "SAGE_ERR_INVALID_ARG", 2: "SAGE_ERR_UNSUPPORTED", 3: "SAGE_ERR_ALIGNMENT",

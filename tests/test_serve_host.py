@@ -2,10 +2,14 @@
 message; the Python layer checks layouts that the C ABI cannot see."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x10000   # aligned, never dereferenced
 
 
@@ -328,3 +332,25 @@ def test_a_workspace_serves_fewer_and_shorter_sequences(adt, Hq, Hk, D):
                     p = adt.SageToken(b, Hq, 0, 0, 0, FAKE, 4096, FAKE, x, 0.0)
                     st = adt._lib.sage_attn_token(FAKE, ctypes.byref(p), c, FAKE, None, FAKE << 8 if ws else None, ws, None)
                     assert st == 4, (B, L, b, x)
+
+
+def test_the_library_serves_without_the_extension_module(adt):
+    """The quantized attention needs libsage.so alone; a serving call names what is missing and how to build it."""
+    code = """if True:
+        import sys
+        sys.modules["action_diffusion_transformers_b200._serve_ext"] = None        # fails to import
+        import torch, action_diffusion_transformers_b200 as adt
+        assert adt.npad(130) == 256 and adt.RopePlan(64).rot_dim == 64
+        x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+        c = adt.KVCache(1, 16, 2, 64, device="cpu")
+        for call in (lambda: adt.sage_attn_prompt(x, x, x, [0, 1]), lambda: c.write(x, x, torch.zeros(1).long()),
+                     lambda: adt.sage_rope(x, x, torch.zeros(1).long(), adt.RopePlan(64))):
+            try:
+                call()
+                assert False
+            except ImportError as e:
+                assert "_serve_ext" in str(e) and "build" in str(e)
+        print("fine")
+    """
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
