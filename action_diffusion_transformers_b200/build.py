@@ -13,6 +13,7 @@ headers into _serve_ext.so, which is linked to libsage.so beside it.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -48,6 +49,12 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def built_for() -> str:
+    """What the extension module depends on besides its sources: the torch and the
+    Python whose interfaces it was compiled against.  The module carries this text."""
+    return f"torch {importlib.metadata.version('torch')}, {sysconfig.get_config_var('SOABI')}"
+
+
 def ext_command(out: str) -> list:
     """g++ command of the extension module.  It leaves the torch libraries to be
     found where `import torch` has loaded them, and libsage.so beside itself."""
@@ -56,7 +63,7 @@ def ext_command(out: str) -> list:
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE]
     return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DSAGE_BUILT_FOR="{built_for()}"']
             + [f for d in inc for f in ("-isystem", d)] + [EXT_SOURCE, "-o", out, "-L", os.path.join(root, "lib")]
             + ["-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-L", PKG, "-l:libsage.so", "-Wl,-rpath,$ORIGIN"])
 
@@ -65,6 +72,9 @@ def up_to_date() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(EXT):
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    with open(EXT, "rb") as f:
+        if built_for().encode() + b"\0" not in f.read():
+            return False
     return all(os.path.getmtime(d) <= t for d in deps())
 
 

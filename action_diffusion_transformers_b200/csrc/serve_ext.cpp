@@ -385,7 +385,7 @@ PyMethodDef kMethods[] = {
     {"attn_token", reinterpret_cast<PyCFunction>(py_token), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_serve_ext", "Serving calls of libsage.so on torch tensors.", -1, kMethods,
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_serve_ext", "Serving calls of libsage.so on torch tensors.  Built for " SAGE_BUILT_FOR, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

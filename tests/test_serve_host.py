@@ -1,6 +1,7 @@
 """The serving calls on the host (no GPU needed): every refusal comes before any CUDA call, with its status and a
 message; the Python layer checks layouts that the C ABI cannot see."""
 import ctypes
+import importlib.util
 import math
 import os
 import subprocess
@@ -354,3 +355,14 @@ def test_the_library_serves_without_the_extension_module(adt):
     """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def test_the_extension_module_is_built_again_for_another_torch(adt, monkeypatch):
+    spec = importlib.util.spec_from_file_location("_build_of_the_module", os.path.join(os.path.dirname(adt.LIB_PATH), "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    assert b.up_to_date()
+    assert torch.__version__ in b.built_for() and adt._serve_ext.__doc__.endswith(b.built_for())
+    for other in (b.built_for() + ".1", b.built_for().replace("torch 2", "torch 3"), "torch 1.0"):
+        monkeypatch.setattr(b, "built_for", lambda other=other: other)
+        assert not b.up_to_date()
