@@ -339,8 +339,9 @@ class RopePlan:
                 self.struct.turns[i] = float(f) / 6.283185307179586
         if mscale is not None:
             self.struct.mscale = float(mscale)
-        self.address = ctypes.addressof(self.struct)
 
+    # Asked for at each call: a copied or unpickled plan has a struct of its own.
+    address = property(lambda self: ctypes.addressof(self.struct))
     n_axes = property(lambda self: self.struct.n_axes)
     rot_dim = property(lambda self: self.struct.rot_dim)
 

@@ -1,9 +1,11 @@
 """The serving calls on the host (no GPU needed): every refusal comes before any CUDA call, with its status and a
 message; the Python layer checks layouts that the C ABI cannot see."""
+import copy
 import ctypes
 import importlib.util
 import math
 import os
+import pickle
 import subprocess
 import sys
 
@@ -366,3 +368,13 @@ def test_the_extension_module_is_built_again_for_another_torch(adt, monkeypatch)
     for other in (b.built_for() + ".1", b.built_for().replace("torch 2", "torch 3"), "torch 1.0"):
         monkeypatch.setattr(b, "built_for", lambda other=other: other)
         assert not b.up_to_date()
+
+
+def test_a_copied_plan_is_its_own(adt):
+    """Plans travel with the modules that hold them: a copy names its own struct, not the first one's (which may be gone)."""
+    first = _plan(adt, 64, scaling="yarn", factor=4.0, orig_len=256)
+    for again in (copy.deepcopy(first), pickle.loads(pickle.dumps(first))):
+        assert again.address == ctypes.addressof(again.struct) != first.address
+        assert bytes(again.struct) == bytes(first.struct)
+        again.struct.mscale = 2.0
+        assert first.struct.mscale != 2.0
