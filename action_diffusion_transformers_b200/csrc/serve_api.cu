@@ -703,6 +703,8 @@ sage_status sage_attn_token(const void* q, const sage_token* a, sage_kv_cache ca
   if (a->B == 0) return SAGE_OK;
   SAGE_NEED(q, "q");
   SAGE_NEED(out, "out");
+  if (q == out && a->B > 1 && p.q_stride != p.out_stride)
+    return fail(SAGE_ERR_INVALID_ARG, "in place, q_stride and out_stride must be equal");
   if (!a->lens) return fail(SAGE_ERR_INVALID_ARG, "lens is NULL");
   if (a->max_len > 0 && !a->page_table) return fail(SAGE_ERR_INVALID_ARG, "page_table is NULL");
   if ((reinterpret_cast<uintptr_t>(a->lens) | reinterpret_cast<uintptr_t>(a->page_table) |

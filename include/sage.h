@@ -459,7 +459,7 @@ SAGE_API sage_status sage_attn_prompt(const void* q, const void* k, const void* 
  *      of a row count, the others may hold anything.  max_len: an upper bound on lens, at most
  *      table_stride * page_size (longer lens are cut there and recorded); it
  *      sets the launch and the workspace.  sm_scale <= 0 selects 1/sqrt(D).
- * out: out [B, Hq, D] of q's type; lse f32 [B, Hq] or NULL; zeros and -inf for a
+ * out: out [B, Hq, D] of q's type, apart from q or q itself (with its stride); lse f32 [B, Hq] or NULL; zeros and -inf for a
  *      sequence without keys.  A page outside the cache is left out and
  *      recorded.  A head of q that holds a NaN or an infinity, and one that sees a
  *      key whose K scale is a NaN, has no softmax: its out and lse are NaN.  A V

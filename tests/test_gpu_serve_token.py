@@ -278,3 +278,15 @@ def test_a_query_that_is_no_number(adt, bad):
             assert bool(torch.isnan(out[b, h]).all()) and bool(torch.isnan(lse[b, h]))
             out[b, h] = clean[b, h]
         assert torch.equal(out, clean) and bool((out[2] == 0).all())      # without keys: zeros
+
+
+@pytest.mark.parametrize("lens", [[70, 0, 300], [9000]])
+def test_in_place(adt, lens):
+    """out may be q: with the keys in one chunk, and in many."""
+    cache, q, table, ln, slots = _setup(adt, lens, 8, 2, 64, 16, "int8", torch.bfloat16, seed=23)
+    ws = _workspace(adt, q, cache, table)
+    want = cache.attend(q, table, ln, torch.empty_like(q.contiguous()), ws)
+    got = q.clone()
+    assert cache.attend(got, table, ln, got, ws) is got
+    adt.sage_check()
+    assert torch.equal(got, want)

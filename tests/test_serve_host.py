@@ -378,3 +378,11 @@ def test_a_copied_plan_is_its_own(adt):
         assert bytes(again.struct) == bytes(first.struct)
         again.struct.mscale = 2.0
         assert first.struct.mscale != 2.0
+
+
+def test_token_attention_in_place_needs_one_stride(adt):
+    c = _cache(adt)
+    for qs, os_, status in ((256, 512, 1), (0, 512, 1), (512, 256, 1)):
+        p = adt.SageToken(2, 4, qs, os_, 0, FAKE, 40, FAKE, 640, 0.0)
+        assert adt._lib.sage_attn_token(FAKE, ctypes.byref(p), c, FAKE, None, FAKE << 8, 1 << 30, None) == status
+        assert b"stride" in adt._lib.sage_last_error()
