@@ -16,15 +16,15 @@
 // An item alone (a pair without its second, or one that the host parts because its
 // end would stand out) gives its key tiles to A and B in turn, each with a ring of
 // its own, and the two results are joined at the end: 1024 tokens x 24 heads 25.7
-// to 19.4 us, chunks of 32 to 1504 tokens behind up to 3000 earlier ones x 24 heads
-// 112.5 to 98.  (K of A and B loaded before V of either, 3 slots each: in the
+// to 19.4 us (16.5 since), chunks of 32 to 1504 tokens behind up to 3000 earlier ones
+// x 24 heads 112.5 to 98 in short runs (104 in a long one).  (K of A and B loaded before V of either, 3 slots each: in the
 // order K, V of A, K, V of B with 2 slots, A's products held up B's next K; 128
 // queries over 8192 keys took 41 instead of 31 us.)
 // Where the items are few, each is given to a cluster of 2 to 8 CTAs, its key
 // tiles dealt out among all their tiles A and B, and the CTAs' results are joined
 // through distributed shared memory in a fixed order (kCluster): 128 queries over
-// 8192 keys x 16 heads 119 to 27 us, x 4 heads 21, one head of 6000 tokens 88 to 38.
-// (The join is the softmax warps' own: behind the point where all warps meet, the
+// 8192 keys x 16 heads 119 to 27 us, x 4 heads 20, one head of 6000 tokens 88 to 37.
+// (The join is the softmax warps' own: behind a point that all warps share, the
 // compiler keeps to the 56 registers of the others, and the chunk took 30 us.)
 //
 // 384 threads:
@@ -68,9 +68,10 @@
 // bring the first two into the row's sum (2^NaN, 2^(inf - inf)), which stays a NaN.
 //
 // Bound by a row tile's chain (scores, softmax, weights, products) with two tiles
-// per SM: 8192 tokens x 32 heads, D = 128, take 536 to 545 us (1010 to 1025 TFLOP/s;
-// 585 us in a long run under the power cap), the tensor pipe 43% and the special-
-// function unit 38% busy; D = 64 400 us, the special-function unit 52%.
+// per SM: 8192 tokens x 32 heads, D = 128, take 529 to 542 us in short runs (1014 to
+// 1040 TFLOP/s) and 577 to 593 in long ones under the power cap (927 to 952), the
+// tensor pipe 44% and the special-function unit 45% busy; D = 64 390 to 430 us, the
+// special-function unit 59%.
 //
 // Every wait on a load or a product is bounded (see mbar_wait_bounded), as in
 // sage_attn.cuh.  The barriers of the softmax warps, of the CTA and of a cluster have
@@ -620,7 +621,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // Up to here nothing of the caller's was read: the set-up above may run beside
-  // the kernel before.
+  // the kernel before.  (On an SM of its own: this CTA's 384 x 168 registers leave
+  // room for no other that wants TMEM, so none of that kernel's can wait for the
+  // columns held here while this CTA waits for it.)
   pdl_enter();
 
   if (warp >= kPrWarpMma) {

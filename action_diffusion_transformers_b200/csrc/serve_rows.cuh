@@ -181,7 +181,8 @@ __device__ __forceinline__ float2 rope_turn(double pos, double turns, float msca
 // pairs are dealt to its lanes in turn, kBatch of them in flight per thread.
 // Bound by HBM: 20480 tokens x 48 heads x 128 (504 MB) take 84 to 89 us, 5.7 to 6.0
 // TB/s against a copy's 6.5, issue 65%; half of 128 channels of 16381 tokens x 36
-// heads 53 to 56 us.
+// heads 53 to 56 us.  V = 1, for halves that are no multiple of 4 channels: 129 us
+// where V = 4 takes 63 (16384 tokens x 40 heads, 18 and 20 pairs; FP32 133 and 115).
 template <class E, bool kHalf, int V>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   pdl_enter();
@@ -353,8 +354,8 @@ __device__ __forceinline__ uint32_t kv_codes4(float a, float b, float c, float d
 // the inverse, in one instruction stream, and both are shuffled out.  With 8
 // channels per lane the per-row work (index, maximum, division) was issued twice
 // as often and bound the kernel (issue 77% busy): 50.9 us for 32768 tokens x 8
-// heads of bf16, against 31 us of HBM time; now 35.9 to 37.5 us, 5.4 to 5.7 TB/s,
-// issue 72%.
+// heads of bf16, against 31 us of HBM time; now 35.6 to 37.8 us, 5.4 to 5.7 TB/s,
+// issue 72%; FP32 59 us, 5.7 TB/s.
 constexpr int kKvPer = 16;
 template <class E>
 constexpr int kKvPiece = 16 / static_cast<int>(sizeof(typename E::S));   // channels of a piece
@@ -455,7 +456,8 @@ __device__ __forceinline__ void kv_values4(uint32_t c, float (&f)[4]) {
 // L = D / 16 lanes per row, 16 codes each, kRows rows in flight per thread.  A
 // lane's channels lie in pieces of 16 result bytes, L pieces side by side, so
 // that each store covers whole sectors (16 channels in a run: 42.0 us for 32768
-// tokens x 8 heads to bf16, against 34.5 to 35.9, 5.7 to 5.9 TB/s).  grid.y: K, V.
+// tokens x 8 heads to bf16, against 34.5 to 36.1, 5.6 to 5.9 TB/s; FP32 57 us).
+// grid.y: K, V.
 template <class E, int D, int kFmt>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const __grid_constant__ KvRowsParams p) {
   pdl_enter();

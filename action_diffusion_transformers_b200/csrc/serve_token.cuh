@@ -32,12 +32,15 @@
 // far below a bf16 output's own (2^-8), but equal to an fp16 output's: there P goes
 // in as two f16 parts (kFine), what the first leaves out being the second, which
 // takes the error against 64 bits from 1.4 times that of the output's rounding to
-// 1.0 times, for 2% of the time (64 sequences of 300 to 8192 keys 102.8 to 105.1
-// us; INT8 codes 107 to 112).  Sums, row maxima and the output stay in 32 bits.
+// 1.0 times, for 3 to 9% of the time (64 sequences of 300 to 8192 keys 103.1 to 106.5
+// us; INT8 codes 110.4 to 120.6).  Sums, row maxima and the output stay in 32 bits.
 //
-// 64 sequences of 300 to 8192 keys x 8 KV heads (D = 128, E4M3, 583 MB) take 103 to
-// 105 us with the join, 5.5 to 5.7 TB/s; ALU 53% and issue 51% busy with turning
-// codes into f16.  One sequence of 3999 keys takes 8.3 us, two launches' latency.
+// 64 sequences of 300 to 8192 keys x 8 KV heads (D = 128, E4M3, 583 MB) take 102 to
+// 113 us with the join, by the lengths and places of their pages, 5.2 to 5.7 TB/s; ALU
+// 52% and issue 51% busy with turning codes into f16.  16 query heads to a KV head
+// (NT = 2, 168 registers and up to 56 bytes of spills) take 143 us where 4 take 103:
+// twice the softmax and products, the tensor pipe 29%; 32, which read every code once
+// per 16, 251.  One sequence of 3999 keys takes 8.5 us, two launches' latency.
 //
 // A CTA takes one chunk of keys of one segment (a sequence and a KV head with up
 // to 8 * NT of its query heads); its warps take 32-key tiles in turn and are
