@@ -35,12 +35,12 @@
 // 1.0 times, for 3 to 9% of the time (64 sequences of 300 to 8192 keys 103.1 to 106.5
 // us; INT8 codes 110.4 to 120.6).  Sums, row maxima and the output stay in 32 bits.
 //
-// 64 sequences of 300 to 8192 keys x 8 KV heads (D = 128, E4M3, 583 MB) take 102 to
-// 113 us with the join, by the lengths and places of their pages, 5.2 to 5.7 TB/s; ALU
+// 64 sequences of 300 to 8192 keys x 8 KV heads (D = 128, E4M3, 583 MB) take 98 to
+// 113 us with the join, by the lengths and places of their pages, 5.2 to 5.9 TB/s; ALU
 // 52% and issue 51% busy with turning codes into f16.  16 query heads to a KV head
-// (NT = 2, 168 registers and up to 56 bytes of spills) take 143 us where 4 take 103:
+// (NT = 2, 168 registers and up to 64 bytes of spills) take 138 us where 4 take 103:
 // twice the softmax and products, the tensor pipe 29%; 32, which read every code once
-// per 16, 251.  One sequence of 3999 keys takes 8.5 us, two launches' latency.
+// per 16, 244.  One sequence of 3999 keys takes 8.5 us, two launches' latency.
 //
 // A CTA takes one chunk of keys of one segment (a sequence and a KV head with up
 // to 8 * NT of its query heads); its warps take 32-key tiles in turn and are
@@ -152,30 +152,29 @@ struct TokQueue {
 };
 
 // Page table entries of the two halves of a tile at `key` of its sequence, as
-// read; kTokNoKey behind the last key.  They are looked at only when the tile's
-// copies start, a tile later, so that the read is not waited for.
-constexpr int kTokNoKey = -0x7FFFFFFF - 1;
+// read; -1 from key `end` on.  They are looked at only when the tile's copies
+// start, a tile later, so that the read is not waited for.
 struct TokPages {
   int page[2];
 };
-__device__ __forceinline__ void tok_cut(TokPages& r, int key, int len) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (key + 16 * h >= len) r.page[h] = kTokNoKey;
-}
-__device__ __forceinline__ TokPages tok_pages(const TokenParams& p, const int32_t* table, int key, int len) {
+__device__ __forceinline__ TokPages tok_pages(const TokenParams& p, const int32_t* table, int key, int end) {
   TokPages r;
 #pragma unroll
   for (int h = 0; h < 2; ++h)      // 16-key halves start at multiples of 16, pages hold a multiple of 16 slots
-    r.page[h] = key + 16 * h < len ? table[(key + 16 * h) >> p.page_shift] : kTokNoKey;
+    r.page[h] = key + 16 * h < end ? table[(key + 16 * h) >> p.page_shift] : -1;
   return r;
+}
+__device__ __forceinline__ void tok_cut(TokPages& r, int key, int end) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (key + 16 * h >= end) r.page[h] = -1;
 }
 
 // Starts the copies of the tile at `key` into a stage (one group per tile, empty
 // where there is nothing to copy); returns which halves have a page.
 template <int D>
-__device__ __forceinline__ int tok_issue(uint32_t stage, const TokenParams& p, const TokPages& pages, int key, int hk,
-                                         int lane) {
+__device__ __forceinline__ int tok_issue(uint32_t stage, const TokenParams& p, const TokPages& pages, int key, int end,
+                                         int hk, int lane) {
   using Q = TokQueue<D>;
   int have = 0;
 #pragma unroll
@@ -194,7 +193,7 @@ __device__ __forceinline__ int tok_issue(uint32_t stage, const TokenParams& p, c
       // lanes 0-15: the K scales of the half, lanes 16-31: its V scales
       cp_async<4>(stage + Q::kScales + ((lane >> 4) * 32 + h * 16 + (lane & 15)) * 4,
                   (lane < 16 ? p.k_scale : p.v_scale) + row + (lane & 15));
-    } else if (pages.page[h] != kTokNoKey) {
+    } else if (key + 16 * h < end) {
       atomicExch(p.err, 1);
     }
   }
@@ -420,7 +419,7 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
   const int tile0 = blockIdx.x * p.per;
   {
     // The length, the pages of the warp's first two tiles and its part of Q are
-    // read side by side; pages behind the length are dropped once it is there.
+    // read side by side; pages behind the chunk's keys are dropped once it is there.
     int tile = tile0 + warp;
     const int all = p.lens[b];
     TokPages pg = tok_pages(p, table, tile * kTokTile, warp < p.per ? p.max_len : 0);
@@ -440,9 +439,10 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
     const int len = min(max(all, 0), p.max_len);
     const int tiles = (len + kTokTile - 1) / kTokTile, tile1 = min(tiles, tile0 + p.per);
     if (tile0 >= tiles && (p.chunks > 1 || blockIdx.x > 0)) return;
-    tok_cut(pg, tile * kTokTile, len);
-    tok_cut(next, (tile + kTokWarps) * kTokTile, len);
-    int have = tok_issue<D>(qaddr, p, pg, tile * kTokTile, hk, lane);
+    const int end = min(len, tile1 * kTokTile);                   // of the chunk's keys
+    tok_cut(pg, tile * kTokTile, end);
+    tok_cut(next, (tile + kTokWarps) * kTokTile, end);
+    int have = tok_issue<D>(qaddr, p, pg, tile * kTokTile, end, hk, lane);
 
     // Q fragments (heads g of each block of 8) and the factor of the scores.
     uint32_t q[NT][D / 16][2];
@@ -496,8 +496,9 @@ __global__ void __launch_bounds__(kTokThreads, kTokPerSm) token_attn_kernel(cons
     }
     static_assert(kTokStages == 2, "the loop keeps one tile ahead");
     for (int stage = 0; tile < tile1; tile += kTokWarps, stage ^= 1) {
-      const int then = tok_issue<D>(qaddr + (stage ^ 1) * Q::kStage, p, next, (tile + kTokWarps) * kTokTile, hk, lane);
-      next = tok_pages(p, table, (tile + 2 * kTokWarps) * kTokTile, tile + 2 * kTokWarps < tile1 ? len : 0);
+      const int then = tok_issue<D>(qaddr + (stage ^ 1) * Q::kStage, p, next, (tile + kTokWarps) * kTokTile, end, hk,
+                                     lane);
+      next = tok_pages(p, table, (tile + 2 * kTokWarps) * kTokTile, end);
       cp_async_wait<1>();
       __syncwarp();        // the other lanes' copies too
       if (have)

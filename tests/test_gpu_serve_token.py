@@ -290,3 +290,18 @@ def test_in_place(adt, lens):
     assert cache.attend(got, table, ln, got, ws) is got
     adt.sage_check()
     assert torch.equal(got, want)
+
+
+def test_any_page_outside_the_cache_is_reported(adt):
+    """The lowest int32 too, in each half of a tile; in entries behind the length nothing is."""
+    lens, ps = [64, 40], 16
+    cache, q, table, ln, slots = _setup(adt, lens, 2, 1, 64, ps, "int8", torch.bfloat16, seed=24)
+    ws = _workspace(adt, q, cache, table)
+    out = torch.empty_like(q.contiguous())
+    want = cache.attend(q, table, ln, torch.empty_like(out), ws)
+    for entry, value, status in ((1, -2 ** 31, 1), (2, -2 ** 31, 1), (3, 2 ** 31 - 1, 1), (4, -2 ** 31, 0), (4, 2 ** 31 - 1, 0)):
+        bad = table.clone()
+        bad[0, entry] = value
+        cache.attend(q, bad, ln, out, ws)
+        assert adt.sage_check_status() == status, (entry, value)
+        assert torch.equal(out[1], want[1]) and torch.equal(out[0], want[0]) == (status == 0)
