@@ -226,6 +226,9 @@ __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, volatile
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, tmo));
 }
 
+// All warps of the CTA, each whole: from different places in the code, which
+// __syncthreads() would not promise.
+__device__ __forceinline__ void pr_meet() { asm volatile("bar.sync 0, %0;" ::"n"(kPrThreads) : "memory"); }
 // All threads of all CTAs of the cluster, each warp whole.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -752,7 +755,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
    }
    __syncwarp();
    tc_fence_before();
-   __syncthreads();
+   pr_meet();
    if (warp == kPrWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    pr_meet();
     if (*abort_flag && tid == 0) atomicExch(p.err, 1);
     const uint32_t todo = prompt_marked<D>(smem)[warp];
     if (todo) prompt_rows_again<E, D>(p, *prompt_marks<D>(smem, x), todo);
